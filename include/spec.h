@@ -86,8 +86,13 @@ enum {
   SPEC_DEV_OVERFLOW = 32,   /* more near-boundary decisions than list slots   */
   SPEC_DEV_BAD_CONF = 64,   /* a confidence logit not finite, or a confidence
                                outside [0, 1] given to the scheduler           */
-  SPEC_DEV_BAD_TREE = 128   /* a tree slot whose parent does not precede it, or
+  SPEC_DEV_BAD_TREE = 128,  /* a tree slot whose parent does not precede it, or
                                deeper than gamma                                */
+  SPEC_DEV_NO_PAGES = 256,  /* a request found no free pages (or no rows) for its
+                               new tokens                                       */
+  SPEC_DEV_BAD_SLOT = 512,  /* a slot or page id outside the cache              */
+  SPEC_DEV_BAD_LOGIT = 1024,/* a row of logits with a NaN, +inf, or only -inf   */
+  SPEC_DEV_BAD_KV = 2048    /* a key or value to be stored that is not finite   */
 };
 
 /* ---------------------------------------------------------------- draft */
@@ -422,6 +427,172 @@ typedef struct {
 } spec_tree_verify_args;
 int32_t spec_tree_verify(const spec_tree_verify_args* args, spec_stream_t stream);
 size_t spec_tree_workspace_bytes(int32_t B, int32_t N, int32_t V);
+
+/* --------------------------------------------- the target model's cache */
+/* No counterpart formulas on the pages beyond the cycle's "target pass over
+ * gamma + 1 positions" and "truncate_kv_cache" ("Speculative Decoding Part 1",
+ * VESSL AI blog, section "알고리즘", pseudo-code): these calls are the target
+ * side of a cycle on a paged cache.  One step of a server is
+ * spec_block_tables (keep what the last verification accepted, make room for
+ * the next block), per layer spec_cache_append and spec_cache_attention,
+ * then spec_verify, then spec_logprobs of the emitted tokens.
+ *
+ * The cache holds keys and values in 4 bits: uint8
+ * [num_pages][Hkv][page_size / 16][18 D].  Each block of 16 tokens of one
+ * key-value head is K codes [16][D/2], K scales [16][D/16], V codes [16][D/2],
+ * V scales [16][D/16].  A code is s e e m (sign, two exponent bits, one
+ * mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6), element 2i in the low half of
+ * byte i; each 16 consecutive elements share one scale byte (0 eeee mmm, bias
+ * 7, the largest 448).  A key stands for code * scale * k_scale, a value for
+ * code * scale * v_scale (k_scale, v_scale: one per layer, in [2^-60, 2^60]).
+ * The product code * scale has six significant bits, exact in 16-bit floats.
+ *
+ * Slot s is token s % page_size of page s / page_size.  page_size is 16, 32,
+ * 64 or 128; D is 64, 128 or 256; num_pages * page_size < 2^31.
+ * dev_status bits are OR-ed in and never cleared by these calls.            */
+size_t spec_cache_bytes(int32_t num_pages, int32_t Hkv, int32_t page_size, int32_t D);
+
+/* spec_block_tables: block tables and slot maps from request lengths, in one
+ * launch.  Request b keeps base = seq_len + accept_len + 1 tokens (accept_len
+ * as spec_verify wrote it; -1 keeps nothing new; a NULL accept_len array
+ * keeps seq_len) and appends new_len tokens; new_len = -1 is a finished
+ * request, which keeps nothing.  kv_len = base + new_len tokens need
+ * ceil(kv_len / page_size) pages: missing ones are taken from the ring of
+ * free pages in request order, surplus ones go back to it in request order.
+ * The ring holds the free pages at entries head .. tail - 1 (mod num_pages);
+ * pages given back in a call are not taken in the same call.  From the first
+ * request on whose pages are not there, or whose rows do not fit max_rows,
+ * every request that would append is refused (SPEC_DEV_NO_PAGES): it keeps
+ * its base tokens and appends none.  A request with a negative length or
+ * page count, new_len < -1, more pages than table_stride, or more kept tokens
+ * than its pages hold sets SPEC_DEV_BAD_LEN: its pages stay, kv_len = 0, no
+ * rows; a page id outside [0, num_pages) sets SPEC_DEV_BAD_SLOT and the
+ * row's slot is -1.
+ * Row i of the packed rows (request order, row_ptr) is token positions[i] of
+ * its request at slot slots[i]; rows from row_ptr[B] to max_rows get -1.
+ * Table entries at and beyond num_blocks_out are left as they are, so a call
+ * repeated on the same inputs gives the same result.  The *_out arrays must
+ * not be the inputs: a server alternates two sets.
+ * Requires 1 <= B <= 4096, 1 <= table_stride, B * table_stride < 2^31,
+ * 1 <= max_rows < 2^31 - 2^20.                                              */
+typedef struct {
+  int32_t B, page_size, num_pages, table_stride, max_rows;
+  const int32_t* seq_len;     /* [B] tokens held before the last block          */
+  const int32_t* accept_len;  /* optional [B], -1 .. : accepted of the last block */
+  const int32_t* new_len;     /* [B] tokens to append; -1 = finished            */
+  const int32_t* num_blocks;  /* [B] pages held                                 */
+  const int64_t* ring_pos;    /* [2] head, tail of the free ring                */
+  int32_t* free_ring;         /* [num_pages] in/out: entries from tail on are written */
+  int32_t* block_table;       /* [B][table_stride] in/out                       */
+  int32_t* seq_len_out;       /* out [B] base                                   */
+  int32_t* kv_len;            /* out [B] base + appended                        */
+  int32_t* num_blocks_out;    /* out [B]                                        */
+  int64_t* ring_pos_out;      /* out [2]                                        */
+  int32_t* row_ptr;           /* out [B+1] first packed row of each request     */
+  int32_t* slots;             /* out [max_rows]                                 */
+  int32_t* positions;         /* out [max_rows]                                 */
+  uint32_t* dev_status;       /* uint32_t[4]; bits OR-ed into [0]               */
+} spec_block_tables_args;
+int32_t spec_block_tables(const spec_block_tables_args* args, spec_stream_t stream);
+
+/* spec_cache_append: rounds T new keys and values to 4 bits and writes them
+ * at their slots (-1: the row is skipped).  Per 16 elements the scale is the
+ * 8-bit float nearest max|x| / (6 g) (g = k_scale or v_scale; at most 448,
+ * ties to even), the codes are the levels nearest x / (scale g) (ties to the
+ * even code, both divisions and products rounded in fp32); a scale that
+ * rounds to 0 stores zeros.  NaN is stored as 0 and an infinity as the
+ * group's largest level under the largest scale, both with SPEC_DEV_BAD_KV.
+ * k_stored / v_stored (optional) receive the values as stored, in dtype,
+ * zeros for skipped rows.  A slot outside the cache sets SPEC_DEV_BAD_SLOT and
+ * its row is skipped; two rows with one slot leave either's token there.
+ * k, v: rows of Hkv heads of D elements, row and head strides in elements
+ * (multiples of 8 for bf16, of 4 for fp32).  1 <= Hkv <= 256, 0 <= T < 2^24. */
+typedef struct {
+  int32_t T, Hkv, D, dtype;
+  int32_t page_size, num_pages;
+  const void* k;              /* [T][Hkv][D] by the strides                     */
+  const void* v;
+  int64_t k_row_stride, k_head_stride, v_row_stride, v_head_stride;
+  const int32_t* slots;       /* [T]                                            */
+  float k_scale, v_scale;
+  uint8_t* cache;
+  void* k_stored;             /* optional out [T][Hkv][D] (dtype)               */
+  void* v_stored;             /* optional out [T][Hkv][D] (dtype)               */
+  uint32_t* dev_status;
+} spec_cache_append_args;
+int32_t spec_cache_append(const spec_cache_append_args* args, spec_stream_t stream);
+
+/* spec_cache_attention: attention of each request's new tokens over its
+ * cache, out = softmax(softmax_scale q K^T) V for every query head (query
+ * head i reads key-value head i / (Hq / Hkv)).  Request b's queries are the
+ * packed rows row_ptr[b] .. row_ptr[b+1] - 1, the last of its kv_len[b]
+ * tokens (already appended).  Row i of n sees the tokens before the new ones
+ * and, of the new ones, 0..i; or, with tree_mask, those whose bit is set in
+ * tree_mask[row][t / 32] >> (t % 32) (a drafted tree's ancestors and itself;
+ * bits beyond n are ignored).  A row that sees nothing gets out = 0 and
+ * lse = -inf.  lse (optional) is log sum exp of the scaled scores.
+ * Arithmetic: products of 16-bit floats that hold codes * scales exactly and
+ * the queries (bf16: exact; fp32: in two terms, 22 bits), fp32 sums;
+ * probabilities rounded to 11 bits (fp32: 22 bits) for the second product.
+ * The result does not depend on the order in which CTAs run.  A request
+ * whose rows or lengths are out of range (row_ptr not ascending within
+ * [0, T], kv_len beyond table_stride pages or below its rows) sets
+ * SPEC_DEV_BAD_LEN, a page id outside the cache SPEC_DEV_BAD_SLOT; rows that
+ * belong to such a request get NaN.  Rows of q outside row_ptr[0] ..
+ * row_ptr[B] - 1 are neither read nor written.
+ * 1 <= B <= 4096, 0 <= T < 2^24, 1 <= Hkv, Hq <= 256, Hq a multiple of Hkv,
+ * B * table_stride < 2^31, kv_len <= 2^30, q strides as in
+ * spec_cache_append; workspace spec_cache_attention_workspace_bytes(Hq, Hkv,
+ * D) bytes (it does not depend on the lengths), 16-byte aligned.             */
+typedef struct {
+  int32_t B, T, Hq, Hkv, D, dtype;
+  int32_t page_size, num_pages, table_stride, mask_words;
+  const void* q;              /* [T][Hq][D] by the strides                      */
+  int64_t q_row_stride, q_head_stride;
+  const uint8_t* cache;
+  const int32_t* block_table; /* [B][table_stride]                              */
+  const int32_t* kv_len;      /* [B] tokens, the new ones included              */
+  const int32_t* row_ptr;     /* [B+1]                                          */
+  const uint32_t* tree_mask;  /* optional [T][mask_words]                       */
+  float softmax_scale, k_scale, v_scale;
+  void* out;                  /* out [T][Hq][D] (dtype)                         */
+  float* lse;                 /* optional out [T][Hq]                           */
+  uint32_t* dev_status;
+  void* workspace;
+  size_t workspace_bytes;
+} spec_cache_attention_args;
+size_t spec_cache_attention_workspace_bytes(int32_t Hq, int32_t Hkv, int32_t D);
+int32_t spec_cache_attention(const spec_cache_attention_args* args, spec_stream_t stream);
+
+/* --------------------------------------------------- log probabilities */
+/* spec_logprobs: for each row (b, j) of logits with a token >= 0, with
+ * x = logits / T_b (T = 1 without temperature): logprob = x[token] - lse(x),
+ * entropy = -sum p log p (natural logarithms), and the K largest entries in
+ * descending order (equal logits: the lower index first) with their log
+ * probabilities.  token = -1 (spec_verify's padding): the row is not read,
+ * its logprob, entropy and top_logprobs are NaN, its top_ids -1.  The same
+ * outputs, with the bit, for a token < -1 or >= V (SPEC_DEV_BAD_TOKEN), a
+ * temperature not finite and > 0 (SPEC_DEV_BAD_TEMP) and a row that has no
+ * distribution (SPEC_DEV_BAD_LOGIT).  -inf logits have probability 0.
+ * Rows: element (b, j, v) at logits[b * b_stride + j * row_stride + v]; any V
+ * and strides (16-byte aligned base).  1 <= B * n <= 2^20, 1 <= V < 2^24,
+ * 0 <= K <= min(32, V); workspace spec_logprobs_workspace_bytes(B * n, V, K). */
+typedef struct {
+  int32_t B, n, V, K, dtype;
+  const void* logits;
+  int64_t b_stride, row_stride;
+  const int32_t* tokens;      /* [B][n]                                         */
+  const float* temperature;   /* optional [B]                                   */
+  float* logprob;             /* out [B][n]                                     */
+  float* entropy;             /* out [B][n]                                     */
+  int32_t* top_ids;           /* out [B][n][K] (NULL iff K = 0)                 */
+  float* top_logprobs;        /* out [B][n][K] (NULL iff K = 0)                 */
+  uint32_t* dev_status;
+  void* workspace;
+  size_t workspace_bytes;
+} spec_logprobs_args;
+size_t spec_logprobs_workspace_bytes(int32_t rows, int32_t V, int32_t K);
+int32_t spec_logprobs(const spec_logprobs_args* args, spec_stream_t stream);
 
 /* ---------------------------------------------- operating-point report */
 /* The analytic speed-up model of "Speculative Decoding Part 1: 도입 전에 확인해야

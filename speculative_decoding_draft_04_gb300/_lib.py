@@ -21,7 +21,8 @@ SPEC_OPT_TEST_STALL = 7
 SPEC_OPT_DRAFT_KERNEL = 8
 SPEC_OPT_VERIFY_KERNEL = 9
 DEV_BITS = {1: "BAD_TOKEN", 2: "BAD_LEN", 4: "BAD_TEMP", 8: "TIMEOUT", 16: "REFINED",
-            32: "OVERFLOW", 64: "BAD_CONF", 128: "BAD_TREE"}
+            32: "OVERFLOW", 64: "BAD_CONF", 128: "BAD_TREE", 256: "NO_PAGES", 512: "BAD_SLOT",
+            1024: "BAD_LOGIT", 2048: "BAD_KV"}
 
 EXPORTED = ("spec_workspace_bytes", "spec_markov_draft", "spec_markov_draft_static",
             "spec_verify", "spec_status_string",
@@ -29,7 +30,9 @@ EXPORTED = ("spec_workspace_bytes", "spec_markov_draft", "spec_markov_draft_stat
             "spec_num_stages", "spec_operating_point", "spec_acceptance_stats",
             "spec_confidence", "spec_schedule_workspace_bytes", "spec_prefix_schedule",
             "spec_rnn_draft", "spec_tree_select", "spec_tree_draft", "spec_tree_verify",
-            "spec_tree_workspace_bytes", "spec_cycle_host")
+            "spec_tree_workspace_bytes", "spec_cycle_host", "spec_cache_bytes",
+            "spec_block_tables", "spec_cache_append", "spec_cache_attention_workspace_bytes",
+            "spec_cache_attention", "spec_logprobs_workspace_bytes", "spec_logprobs")
 
 
 class SpecError(RuntimeError):
@@ -37,6 +40,7 @@ class SpecError(RuntimeError):
 
 
 _i32, _vp, _sz = ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
+_i64, _f32 = ctypes.c_int64, ctypes.c_float
 
 
 class DraftArgs(ctypes.Structure):
@@ -112,6 +116,41 @@ class TreeVerifyArgs(ctypes.Structure):
                 ("workspace_bytes", _sz)]
 
 
+class BlockTablesArgs(ctypes.Structure):
+    _fields_ = [("B", _i32), ("page_size", _i32), ("num_pages", _i32), ("table_stride", _i32),
+                ("max_rows", _i32), ("seq_len", _vp), ("accept_len", _vp), ("new_len", _vp),
+                ("num_blocks", _vp), ("ring_pos", _vp), ("free_ring", _vp), ("block_table", _vp),
+                ("seq_len_out", _vp), ("kv_len", _vp), ("num_blocks_out", _vp),
+                ("ring_pos_out", _vp), ("row_ptr", _vp), ("slots", _vp), ("positions", _vp),
+                ("dev_status", _vp)]
+
+
+class CacheAppendArgs(ctypes.Structure):
+    _fields_ = [("T", _i32), ("Hkv", _i32), ("D", _i32), ("dtype", _i32), ("page_size", _i32),
+                ("num_pages", _i32), ("k", _vp), ("v", _vp), ("k_row_stride", _i64),
+                ("k_head_stride", _i64), ("v_row_stride", _i64), ("v_head_stride", _i64),
+                ("slots", _vp), ("k_scale", _f32), ("v_scale", _f32), ("cache", _vp),
+                ("k_stored", _vp), ("v_stored", _vp), ("dev_status", _vp)]
+
+
+class CacheAttentionArgs(ctypes.Structure):
+    _fields_ = [("B", _i32), ("T", _i32), ("Hq", _i32), ("Hkv", _i32), ("D", _i32),
+                ("dtype", _i32), ("page_size", _i32), ("num_pages", _i32), ("table_stride", _i32),
+                ("mask_words", _i32), ("q", _vp), ("q_row_stride", _i64), ("q_head_stride", _i64),
+                ("cache", _vp), ("block_table", _vp), ("kv_len", _vp), ("row_ptr", _vp),
+                ("tree_mask", _vp), ("softmax_scale", _f32), ("k_scale", _f32), ("v_scale", _f32),
+                ("out", _vp), ("lse", _vp), ("dev_status", _vp), ("workspace", _vp),
+                ("workspace_bytes", _sz)]
+
+
+class LogprobsArgs(ctypes.Structure):
+    _fields_ = [("B", _i32), ("n", _i32), ("V", _i32), ("K", _i32), ("dtype", _i32),
+                ("logits", _vp), ("b_stride", _i64), ("row_stride", _i64), ("tokens", _vp),
+                ("temperature", _vp), ("logprob", _vp), ("entropy", _vp), ("top_ids", _vp),
+                ("top_logprobs", _vp), ("dev_status", _vp), ("workspace", _vp),
+                ("workspace_bytes", _sz)]
+
+
 def lib(path: str | None = None) -> ctypes.CDLL:
     """Load libspec.so (built in-tree by build.build())."""
     global _LIB
@@ -164,6 +203,20 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     L.spec_schedule_workspace_bytes.argtypes = [_i32, _i32]
     L.spec_prefix_schedule.restype = _i32
     L.spec_prefix_schedule.argtypes = [ctypes.POINTER(ScheduleArgs), _vp]
+    L.spec_cache_bytes.restype = _sz
+    L.spec_cache_bytes.argtypes = [_i32, _i32, _i32, _i32]
+    L.spec_block_tables.restype = _i32
+    L.spec_block_tables.argtypes = [ctypes.POINTER(BlockTablesArgs), _vp]
+    L.spec_cache_append.restype = _i32
+    L.spec_cache_append.argtypes = [ctypes.POINTER(CacheAppendArgs), _vp]
+    L.spec_cache_attention_workspace_bytes.restype = _sz
+    L.spec_cache_attention_workspace_bytes.argtypes = [_i32, _i32, _i32]
+    L.spec_cache_attention.restype = _i32
+    L.spec_cache_attention.argtypes = [ctypes.POINTER(CacheAttentionArgs), _vp]
+    L.spec_logprobs_workspace_bytes.restype = _sz
+    L.spec_logprobs_workspace_bytes.argtypes = [_i32, _i32, _i32]
+    L.spec_logprobs.restype = _i32
+    L.spec_logprobs.argtypes = [ctypes.POINTER(LogprobsArgs), _vp]
     if path is None:
         _LIB = L
     return L
@@ -397,3 +450,129 @@ def spec_tree_verify(target, U, W1, W2, anchor, temperature, parent, mask, token
                        _ptr(out_tokens), _ptr(path), _ptr(dev_status), _ptr(workspace),
                        workspace.numel() * workspace.element_size())
     _check(lib().spec_tree_verify(ctypes.byref(a), _stream(stream)), "spec_tree_verify")
+
+
+# ------------------------------------------------------- target side of a cycle
+
+def _tensor(t, what: str, dtype: str, shape: tuple) -> int:
+    """Address of a contiguous CUDA tensor of this type and shape."""
+    if str(t.dtype) != dtype or tuple(t.shape) != shape:
+        raise SpecError(f"{what} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
+    return _ptr(t)
+
+
+def _heads(t, what: str, T: int, H: int, D: int) -> int:
+    """Address of a CUDA tensor [T][H][D] whose heads are contiguous."""
+    if tuple(t.shape) != (T, H, D) or t.stride(2) != 1:
+        raise SpecError(f"{what} must be [{T}, {H}, {D}] with contiguous heads, not {list(t.shape)} "
+                        f"with strides {list(t.stride())}")
+    if not t.is_cuda:
+        raise SpecError("tensors must be CUDA tensors")
+    return t.data_ptr()
+
+
+def _cache_shape(cache, D: int) -> tuple:
+    """(num_pages, Hkv, page_size) of a 4-bit cache [num_pages][Hkv][page_size / 16][18 D]."""
+    if cache.dim() != 4 or cache.shape[3] != 18 * D or str(cache.dtype) != "torch.uint8":
+        raise SpecError(f"cache must be torch.uint8 [num_pages, Hkv, page_size / 16, {18 * D}], not "
+                        f"{cache.dtype} {list(cache.shape)}")
+    return cache.shape[0], cache.shape[1], cache.shape[2] * 16
+
+
+def spec_cache_bytes(num_pages: int, Hkv: int, page_size: int, D: int) -> int:
+    return int(lib().spec_cache_bytes(num_pages, Hkv, page_size, D))
+
+
+def spec_block_tables(seq_len, accept_len, new_len, num_blocks, ring_pos, free_ring, block_table,
+                      seq_len_out, kv_len, num_blocks_out, ring_pos_out, row_ptr, slots, positions,
+                      dev_status, page_size: int, stream=None) -> None:
+    """Block tables, slots and positions of every request's next tokens
+    (accept_len None: the lengths are final)."""
+    B, i32, i64 = seq_len.shape[0], "torch.int32", "torch.int64"
+    stride, rows = block_table.shape[1], slots.shape[0]
+    a = BlockTablesArgs(
+        B, page_size, free_ring.shape[0], stride, rows, _tensor(seq_len, "seq_len", i32, (B,)),
+        None if accept_len is None else _tensor(accept_len, "accept_len", i32, (B,)),
+        _tensor(new_len, "new_len", i32, (B,)), _tensor(num_blocks, "num_blocks", i32, (B,)),
+        _tensor(ring_pos, "ring_pos", i64, (2,)),
+        _tensor(free_ring, "free_ring", i32, (free_ring.shape[0],)),
+        _tensor(block_table, "block_table", i32, (B, stride)),
+        _tensor(seq_len_out, "seq_len_out", i32, (B,)), _tensor(kv_len, "kv_len", i32, (B,)),
+        _tensor(num_blocks_out, "num_blocks_out", i32, (B,)),
+        _tensor(ring_pos_out, "ring_pos_out", i64, (2,)),
+        _tensor(row_ptr, "row_ptr", i32, (B + 1,)), _tensor(slots, "slots", i32, (rows,)),
+        _tensor(positions, "positions", i32, (rows,)), _tensor(dev_status, "dev_status", i32, (4,)))
+    _check(lib().spec_block_tables(ctypes.byref(a), _stream(stream)), "spec_block_tables")
+
+
+def spec_cache_append(k, v, slots, cache, dev_status, k_scale: float = 1.0, v_scale: float = 1.0,
+                      k_stored=None, v_stored=None, stream=None) -> None:
+    """Round keys and values [T][Hkv][D] to 4 bits into the cache at their
+    slots; k_stored / v_stored receive the values as stored."""
+    T, H, D = k.shape
+    pages, Hkv, P = _cache_shape(cache, D)
+    dt = str(k.dtype)
+    if Hkv != H or v.dtype != k.dtype:
+        raise SpecError(f"k, v and cache disagree: {H} and {Hkv} heads, {k.dtype} and {v.dtype}")
+    a = CacheAppendArgs(
+        T, H, D, _dtype_code(k), P, pages, _heads(k, "k", T, H, D), _heads(v, "v", T, H, D),
+        k.stride(0), k.stride(1), v.stride(0), v.stride(1), _tensor(slots, "slots", "torch.int32", (T,)),
+        k_scale, v_scale, _ptr(cache),
+        None if k_stored is None else _tensor(k_stored, "k_stored", dt, (T, H, D)),
+        None if v_stored is None else _tensor(v_stored, "v_stored", dt, (T, H, D)),
+        _tensor(dev_status, "dev_status", "torch.int32", (4,)))
+    _check(lib().spec_cache_append(ctypes.byref(a), _stream(stream)), "spec_cache_append")
+
+
+def spec_cache_attention_workspace_bytes(Hq: int, Hkv: int, D: int) -> int:
+    return int(lib().spec_cache_attention_workspace_bytes(Hq, Hkv, D))
+
+
+def spec_cache_attention(q, cache, block_table, kv_len, row_ptr, out, dev_status, workspace,
+                         softmax_scale: float, k_scale: float = 1.0, v_scale: float = 1.0,
+                         tree_mask=None, lse=None, stream=None) -> None:
+    """Attention of the packed rows q [T][Hq][D] of every request over its
+    cached tokens; tree_mask [T][words] (int32 bit words) replaces the causal
+    order among a request's new tokens."""
+    T, Hq, D = q.shape
+    B, stride = block_table.shape
+    pages, Hkv, P = _cache_shape(cache, D)
+    words = 0 if tree_mask is None else tree_mask.shape[1]
+    a = CacheAttentionArgs(
+        B, T, Hq, Hkv, D, _dtype_code(q), P, pages, stride, words, _heads(q, "q", T, Hq, D),
+        q.stride(0), q.stride(1), _ptr(cache),
+        _tensor(block_table, "block_table", "torch.int32", (B, stride)),
+        _tensor(kv_len, "kv_len", "torch.int32", (B,)), _tensor(row_ptr, "row_ptr", "torch.int32", (B + 1,)),
+        None if tree_mask is None else _tensor(tree_mask, "tree_mask", "torch.int32", (T, words)),
+        softmax_scale, k_scale, v_scale, _tensor(out, "out", str(q.dtype), (T, Hq, D)),
+        None if lse is None else _tensor(lse, "lse", "torch.float32", (T, Hq)),
+        _tensor(dev_status, "dev_status", "torch.int32", (4,)), _ptr(workspace),
+        workspace.numel() * workspace.element_size())
+    _check(lib().spec_cache_attention(ctypes.byref(a), _stream(stream)), "spec_cache_attention")
+
+
+def spec_logprobs_workspace_bytes(rows: int, V: int, K: int) -> int:
+    return int(lib().spec_logprobs_workspace_bytes(rows, V, K))
+
+
+def spec_logprobs(logits, tokens, logprob, entropy, dev_status, workspace, temperature=None,
+                  top_ids=None, top_logprobs=None, stream=None) -> None:
+    """Log probabilities of tokens [B][n] under logits [B][n][V], the entropies,
+    and the K = top_ids.shape[2] largest entries of each row."""
+    B, n, V = logits.shape
+    f32, i32 = "torch.float32", "torch.int32"
+    K = 0 if top_ids is None else top_ids.shape[2]
+    if logits.stride(2) != 1 or not logits.is_cuda:
+        raise SpecError("logits must be a CUDA tensor with contiguous rows")
+    if (top_ids is None) != (top_logprobs is None):
+        raise SpecError("top_ids and top_logprobs go together")
+    a = LogprobsArgs(
+        B, n, V, K, _dtype_code(logits), logits.data_ptr(), logits.stride(0), logits.stride(1),
+        _tensor(tokens, "tokens", i32, (B, n)),
+        None if temperature is None else _tensor(temperature, "temperature", f32, (B,)),
+        _tensor(logprob, "logprob", f32, (B, n)), _tensor(entropy, "entropy", f32, (B, n)),
+        _tensor(top_ids, "top_ids", i32, (B, n, K)) if K else None,
+        _tensor(top_logprobs, "top_logprobs", f32, (B, n, K)) if K else None,
+        _tensor(dev_status, "dev_status", i32, (4,)), _ptr(workspace),
+        workspace.numel() * workspace.element_size())
+    _check(lib().spec_logprobs(ctypes.byref(a), _stream(stream)), "spec_logprobs")

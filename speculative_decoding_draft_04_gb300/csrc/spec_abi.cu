@@ -64,6 +64,13 @@ cudaError_t launch_tree_verify(const TreeShape&, const void*, const void*, const
                                const float*, const float*, int*, int*, int*, void*, uint32_t*,
                                cudaStream_t);
 
+cudaError_t launch_block_tables(const spec_block_tables_args&, int, cudaStream_t);
+cudaError_t launch_cache_append(const spec_cache_append_args&, int, cudaStream_t);
+size_t cache_attention_workspace_bytes(int, int, int);
+cudaError_t launch_cache_attention(const spec_cache_attention_args&, int, cudaStream_t);
+size_t logprobs_workspace_bytes(int, int, int);
+cudaError_t launch_logprobs(const spec_logprobs_args&, int, cudaStream_t);
+
 // ---------------------------------------------------------------- options
 namespace {
 std::mutex g_mu;
@@ -106,13 +113,13 @@ enum Stage {
   ST_DRAFT_PERSISTENT, ST_DRAFT_SLICE, ST_VERIFY_PREP,
   ST_TARGET_STATS, ST_VERIFY_TILE, ST_VERIFY_SLICE, ST_VERIFY_FINAL, ST_SLOW_VERIFY, ST_VERIFY_HP_SUMS,
   ST_VERIFY_HP_RESID, ST_VERIFY_REDECIDE, ST_CONFIDENCE, ST_SCHED_RANK, ST_SCHED_SELECT, ST_TREE_SELECT,
-  ST_TREE_DRAFT, ST_TREE_VERIFY, ST_COUNT
+  ST_TREE_DRAFT, ST_TREE_VERIFY, ST_BLOCK_TABLES, ST_CACHE_APPEND, ST_CACHE_ATTENTION, ST_LOGPROBS, ST_COUNT
 };
 const char* kStageNames[ST_COUNT] = {
     "draft_persistent", "draft_slice", "verify_prep",
     "target_stats", "verify_tile", "verify_slice", "verify_final", "slow_verify", "verify_hp_sums",
     "verify_hp_resid", "verify_redecide", "confidence", "sched_rank", "sched_select", "tree_select",
-    "tree_draft", "tree_verify"};
+    "tree_draft", "tree_verify", "block_tables", "cache_append", "cache_attention", "logprobs"};
 bool g_prof = false;
 struct EvPair { cudaEvent_t a, b; int stage; };
 std::vector<EvPair> g_pending;
@@ -743,6 +750,134 @@ int32_t spec_prefix_schedule(const spec_schedule_args* a, spec_stream_t stream) 
       return SPEC_ECUDA;
   }
   return SPEC_OK;
+}
+
+// ---------------------------------------------------------------- target side
+namespace {
+bool page_ok(int P) { return P == 16 || P == 32 || P == 64 || P == 128; }
+bool head_ok(int D) { return D == 64 || D == 128 || D == 256; }
+bool cache_scale_ok(float g) { return g >= 0x1p-60f && g <= 0x1p60f; }   // false for NaN
+// A row or head stride in elements: whole 16-byte units.
+bool stride_ok(int64_t s, int dtype) { return s % (dtype == SPEC_BF16 ? 8 : 4) == 0; }
+}  // namespace
+
+size_t spec_cache_bytes(int32_t num_pages, int32_t Hkv, int32_t page_size, int32_t D) {
+  if (num_pages < 1 || Hkv < 1 || Hkv > 256 || !page_ok(page_size) || !head_ok(D) ||
+      (int64_t)num_pages * page_size > 0x7fffffff)
+    return 0;
+  return (size_t)num_pages * Hkv * (page_size / 16) * 18 * D;
+}
+
+int32_t spec_block_tables(const spec_block_tables_args* a, spec_stream_t stream) {
+  if (!a) return SPEC_EINVAL;
+  if (a->B < 1 || a->B > 4096 || a->num_pages < 1 || a->table_stride < 1 || a->max_rows < 1 ||
+      a->max_rows >= 0x7fffffff - (1 << 20) || (int64_t)a->B * a->table_stride > 0x7fffffff ||
+      (int64_t)a->num_pages * a->page_size > 0x7fffffff)
+    return SPEC_EINVAL;
+  if (!page_ok(a->page_size)) return SPEC_EUNSUPPORTED;
+  if (!a->seq_len || !a->new_len || !a->num_blocks || !a->ring_pos || !a->free_ring || !a->block_table ||
+      !a->seq_len_out || !a->kv_len || !a->num_blocks_out || !a->ring_pos_out || !a->row_ptr || !a->slots ||
+      !a->positions || !a->dev_status)
+    return SPEC_EINVAL;
+  // every CTA reads the inputs while CTA 0 writes the outputs
+  const void* in[5] = {a->seq_len, a->accept_len, a->new_len, a->num_blocks, a->ring_pos};
+  const void* out[5] = {a->seq_len_out, a->kv_len, a->num_blocks_out, a->ring_pos_out, a->row_ptr};
+  for (const void* i : in)
+    for (const void* o : out)
+      if (i == o) return SPEC_EINVAL;
+  if (!aligned(a->seq_len, 4) || !aligned(a->accept_len, 4) || !aligned(a->new_len, 4) ||
+      !aligned(a->num_blocks, 4) || !aligned(a->ring_pos, 8) || !aligned(a->free_ring, 4) ||
+      !aligned(a->block_table, 4) || !aligned(a->seq_len_out, 4) || !aligned(a->kv_len, 4) ||
+      !aligned(a->num_blocks_out, 4) || !aligned(a->ring_pos_out, 8) || !aligned(a->row_ptr, 4) ||
+      !aligned(a->slots, 16) || !aligned(a->positions, 16) || !aligned(a->dev_status, 4))
+    return SPEC_EALIGN;
+  const int sms = num_sms();
+  if (sms <= 0) return SPEC_ECUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope p(st, ST_BLOCK_TABLES);
+  return launch_block_tables(*a, sms, st) == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}
+
+int32_t spec_cache_append(const spec_cache_append_args* a, spec_stream_t stream) {
+  if (!a) return SPEC_EINVAL;
+  if (a->T < 0 || a->T >= (1 << 24) || a->Hkv < 1 || a->Hkv > 256 || a->num_pages < 1 ||
+      (int64_t)a->num_pages * a->page_size > 0x7fffffff || !cache_scale_ok(a->k_scale) ||
+      !cache_scale_ok(a->v_scale))
+    return SPEC_EINVAL;
+  if (!page_ok(a->page_size) || !head_ok(a->D) || (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16))
+    return SPEC_EUNSUPPORTED;
+  if (a->T == 0) return SPEC_OK;
+  if (!a->k || !a->v || !a->slots || !a->cache || !a->dev_status) return SPEC_EINVAL;
+  if (!aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(a->slots, 4) || !aligned(a->cache, 16) ||
+      !aligned(a->k_stored, 16) || !aligned(a->v_stored, 16) || !aligned(a->dev_status, 4) ||
+      !stride_ok(a->k_row_stride, a->dtype) || !stride_ok(a->k_head_stride, a->dtype) ||
+      !stride_ok(a->v_row_stride, a->dtype) || !stride_ok(a->v_head_stride, a->dtype))
+    return SPEC_EALIGN;
+  const int sms = num_sms();
+  if (sms <= 0) return SPEC_ECUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope p(st, ST_CACHE_APPEND);
+  return launch_cache_append(*a, sms, st) == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}
+
+size_t spec_cache_attention_workspace_bytes(int32_t Hq, int32_t Hkv, int32_t D) {
+  if (Hkv < 1 || Hq < Hkv || Hq > 256 || Hq % Hkv != 0 || !head_ok(D)) return 0;
+  return cache_attention_workspace_bytes(Hq, Hkv, D);
+}
+
+int32_t spec_cache_attention(const spec_cache_attention_args* a, spec_stream_t stream) {
+  if (!a) return SPEC_EINVAL;
+  if (a->B < 1 || a->B > 4096 || a->T < 0 || a->T >= (1 << 24) || a->Hkv < 1 || a->Hq < a->Hkv ||
+      a->Hq > 256 || a->Hq % a->Hkv != 0 || a->num_pages < 1 || a->table_stride < 1 ||
+      (int64_t)a->B * a->table_stride > 0x7fffffff || (int64_t)a->num_pages * a->page_size > 0x7fffffff ||
+      !cache_scale_ok(a->k_scale) || !cache_scale_ok(a->v_scale) || !isfinite(a->softmax_scale) ||
+      a->mask_words < 0 || (a->tree_mask && a->mask_words < 1))
+    return SPEC_EINVAL;
+  if (!page_ok(a->page_size) || !head_ok(a->D) || (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16))
+    return SPEC_EUNSUPPORTED;
+  if (a->T == 0) return SPEC_OK;
+  if (!a->q || !a->cache || !a->block_table || !a->kv_len || !a->row_ptr || !a->out || !a->dev_status)
+    return SPEC_EINVAL;
+  if (!aligned(a->q, 16) || !aligned(a->cache, 16) || !aligned(a->block_table, 4) || !aligned(a->kv_len, 4) ||
+      !aligned(a->row_ptr, 4) || !aligned(a->tree_mask, 4) || !aligned(a->out, 16) || !aligned(a->lse, 4) ||
+      !aligned(a->dev_status, 4) || !stride_ok(a->q_row_stride, a->dtype) || !stride_ok(a->q_head_stride, a->dtype))
+    return SPEC_EALIGN;
+  if (!a->workspace || a->workspace_bytes < spec_cache_attention_workspace_bytes(a->Hq, a->Hkv, a->D))
+    return SPEC_EWORKSPACE;
+  if (!aligned(a->workspace, 16)) return SPEC_EALIGN;
+  const int sms = num_sms();
+  if (sms <= 0) return SPEC_ECUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope p(st, ST_CACHE_ATTENTION);
+  return launch_cache_attention(*a, sms, st) == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}
+
+size_t spec_logprobs_workspace_bytes(int32_t rows, int32_t V, int32_t K) {
+  if (rows < 1 || rows > (1 << 20) || V < 1 || V >= (1 << 24) || K < 0 || K > 32 || K > V) return 0;
+  return logprobs_workspace_bytes(rows, V, K);
+}
+
+int32_t spec_logprobs(const spec_logprobs_args* a, spec_stream_t stream) {
+  if (!a) return SPEC_EINVAL;
+  if (a->B < 1 || a->n < 1 || (int64_t)a->B * a->n > (1 << 20) || a->V < 1 || a->V >= (1 << 24) || a->K < 0 ||
+      a->K > a->V)
+    return SPEC_EINVAL;
+  if (a->K > 32 || (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16)) return SPEC_EUNSUPPORTED;
+  if (!a->logits || !a->tokens || !a->logprob || !a->entropy || !a->dev_status ||
+      (a->K > 0) != (a->top_ids != nullptr) || (a->K > 0) != (a->top_logprobs != nullptr))
+    return SPEC_EINVAL;
+  if (!aligned(a->logits, 16) || !aligned(a->tokens, 4) || !aligned(a->temperature, 4) ||
+      !aligned(a->logprob, 4) || !aligned(a->entropy, 4) || !aligned(a->top_ids, 4) ||
+      !aligned(a->top_logprobs, 4) || !aligned(a->dev_status, 4))
+    return SPEC_EALIGN;
+  if (!a->workspace || a->workspace_bytes < spec_logprobs_workspace_bytes(a->B * a->n, a->V, a->K))
+    return SPEC_EWORKSPACE;
+  if (!aligned(a->workspace, 16)) return SPEC_EALIGN;
+  const int sms = num_sms();
+  if (sms <= 0) return SPEC_ECUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope p(st, ST_LOGPROBS);
+  return launch_logprobs(*a, sms, st) == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }
 
 // ---------------------------------------------------------------- trees
