@@ -535,12 +535,14 @@ int32_t spec_cache_append(const spec_cache_append_args* args, spec_stream_t stre
  * the queries (bf16: exact; fp32: in two terms, 22 bits), fp32 sums;
  * probabilities rounded to 11 bits (fp32: 22 bits) for the second product.
  * The result does not depend on the order in which CTAs run.  A request
- * whose rows or lengths are out of range (row_ptr not ascending within
- * [0, T], kv_len beyond table_stride pages or below its rows) sets
- * SPEC_DEV_BAD_LEN, a page id outside the cache SPEC_DEV_BAD_SLOT; rows that
- * belong to such a request get NaN.  Rows of q outside row_ptr[0] ..
- * row_ptr[B] - 1 are neither read nor written.
- * 1 <= B <= 4096, 0 <= T < 2^24, 1 <= Hkv, Hq <= 256, Hq a multiple of Hkv,
+ * whose length is out of range (kv_len beyond table_stride pages or below its
+ * rows) sets SPEC_DEV_BAD_LEN, a page id outside the cache SPEC_DEV_BAD_SLOT;
+ * the request's rows (of a bad page: those of its unit's row tile) get NaN.
+ * A request whose row_ptr entries do not ascend within [0, T] sets
+ * SPEC_DEV_BAD_LEN and has no rows.  Rows of q that belong to no request are
+ * neither read nor written.  A bounded wait that gives up sets
+ * SPEC_DEV_TIMEOUT.
+ * 1 <= B <= 4096, 0 <= T < 2^24, T * Hq < 2^31, Hq <= 256 a multiple of Hkv,
  * B * table_stride < 2^31, kv_len <= 2^30, q strides as in
  * spec_cache_append; workspace spec_cache_attention_workspace_bytes(Hq, Hkv,
  * D) bytes (it does not depend on the lengths), 16-byte aligned.             */
