@@ -31,40 +31,9 @@
 // A segment inside one warp's share is written at once.  Otherwise each part is
 // kept as (m, sum, unnormalised out) in the workspace and
 // cache_attention_join_kernel adds the parts in the order of their warps.
-#include "spec_serve.cuh"
-#include "spec_tc.cuh"
+#include "spec_attention.cuh"
 
 namespace spec {
-
-struct AttnParams {
-  int B, T, Hq, Hkv, G, P, num_pages, stride, mask_words;
-  const void* q;
-  long long q_row, q_head;
-  const uint8_t* cache;
-  const int* table;
-  const int* kv_len;
-  const int* row_ptr;
-  const uint32_t* mask;
-  float scale;                            // softmax_scale * k_scale * log2(e)
-  float v_scale;
-  void* out;
-  float* lse;
-  uint32_t* status;
-  void* ws;
-};
-
-constexpr int AT_WARPS = 8;               // warps a CTA at most
-constexpr int AT_UNIT = 32;               // tokens
-constexpr int AT_MAX_CTAS = 2 * 160;      // workspace slots: two CTAs an SM at most
-constexpr float AT_SLACK = 8.f;           // rows are rescaled once p passes 2^(AT_SHIFT + AT_SLACK) ..
-constexpr float AT_SHIFT = 7.f;           // .. which is 2^15, of the 16-bit float's 2^16
-
-// One split segment: the warps first .. last hold its parts.
-struct AttnSplit {
-  int first, last;                        // last < first: no segment is split after this warp
-  int b, h, tile;
-  int n, r0;
-};
 
 // Geometry of a kernel: head size, row tiles of 16, terms of a 16-bit split.
 template <int D_, int M_, int NT_>
@@ -78,108 +47,18 @@ struct AttnCfg {
   static constexpr int VW = D >= 128 ? D / 64 : 1;      // V code words a lane and token (D = 64: 4 bytes)
   static constexpr int UNIT_BYTES = 2 * 18 * D;
   static constexpr int Q_BYTES = NT * M * KSTEPS * 512;
-  static constexpr int MIN_CTAS = (M == 1 && NT == 1 && D <= 128) ? 2 : 1;
-  static constexpr int WARPS = D == 256 && NT == 2 ? 4 : AT_WARPS;
+  // 12 warps of 168 registers where 8 of 255 are not needed; two CTAs of 8 for small heads
+  static constexpr int MIN_CTAS = M == 1 && NT == 1 && D == 64 ? 2 : 1;
+  static constexpr int WARPS = D == 256 && NT == 2 ? 4 : D == 128 && M == 1 && NT == 1 ? 12 : 8;
   static constexpr int WARP_BUDGET = (MIN_CTAS == 2 ? 110 : 220) * 1024 / WARPS;
   static constexpr int FIT = (WARP_BUDGET - Q_BYTES) / UNIT_BYTES;
   static constexpr int DEPTH = FIT > 6 ? 6 : FIT;
   static constexpr int WARP_BYTES = Q_BYTES + DEPTH * UNIT_BYTES;
   static constexpr int SMEM = WARPS * WARP_BYTES;
-  // floats of a part: the accumulators lane by lane, then (m, sum) a row
+  // floats of a part: [ROWS][D] outputs, then (m, sum) a row
   static constexpr int PART = ROWS * D + 2 * ROWS;
   static_assert(DEPTH >= 2, "ring");
 };
-
-// What a segment is: request b's units over key-value head h for one row tile.
-struct AttnSeg {
-  int b, h, tile, u, nu;                  // units u .. nu - 1 are left
-  int n, r0, L;
-  bool bad;
-};
-
-// Units of request b over all heads and row tiles (0: nothing to do).
-template <int ROWS>
-__device__ __forceinline__ long long attn_work(const AttnParams& p, int b, int& n, int& r0, int& L, int& tiles,
-                                               int& nu, bool& bad, bool& outside) {
-  r0 = __ldg(p.row_ptr + b);
-  const int r1 = __ldg(p.row_ptr + b + 1);
-  L = __ldg(p.kv_len + b);
-  n = r1 - r0;
-  outside = r0 < 0 || r1 < r0 || r1 > p.T;
-  bad = false;
-  if (outside || n == 0) {
-    n = 0;
-    tiles = nu = 0;
-    return 0;
-  }
-  bad = L < n || L > (1 << 30) || L > (long long)p.stride * p.P;
-  tiles = (n * p.G + ROWS - 1) / ROWS;
-  nu = bad ? 1 : (L + AT_UNIT - 1) / AT_UNIT;
-  return (long long)p.Hkv * tiles * nu;
-}
-
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-__device__ __forceinline__ void expect_bytes(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void mbar_arrive1(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ void mma_f16(float* c, const uint4& a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float exp2_approx(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-// Byte i (a compile-time constant) of a word array as two 16-bit floats.
-__device__ __forceinline__ uint32_t decode_byte(const uint32_t* w, int i) {
-  switch (i & 3) {
-    case 0: return decode_pair<0>(w[i >> 2]);
-    case 1: return decode_pair<1>(w[i >> 2]);
-    case 2: return decode_pair<2>(w[i >> 2]);
-    default: return decode_pair<3>(w[i >> 2]);
-  }
-}
-
-__device__ __forceinline__ void load4(const bf16* p, float* x) {
-  const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-  x[0] = __uint_as_float(v.x << 16);
-  x[1] = __uint_as_float(v.x & 0xffff0000u);
-  x[2] = __uint_as_float(v.y << 16);
-  x[3] = __uint_as_float(v.y & 0xffff0000u);
-}
-__device__ __forceinline__ void load4(const float* p, float* x) {
-  const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-}
-__device__ __forceinline__ void store4(bf16* p, const float* x) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
-__device__ __forceinline__ void store4(float* p, const float* x) {
-  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-}
 
 // First head element of lane part t in inner step s of the first product.
 template <int D>
@@ -274,136 +153,87 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
   const int g = lane >> 2, t = lane & 3;
   uint64_t* bar = s_bar[warp];
 
-  // ---- units before each group of `items` requests
-  const int items = (p.B + 32 * C::WARPS - 1) / (32 * C::WARPS);
-  long long total;
-  {
-    long long mine = 0;
-    bool flag = false;
-    for (int i = 0; i < items; ++i) {
-      const int b = tid * items + i;
-      if (b >= p.B) break;
-      int n, r0, L, tiles, nu;
-      bool bad, outside;
-      mine += attn_work<C::ROWS>(p, b, n, r0, L, tiles, nu, bad, outside);
-      flag |= bad || outside;
-    }
-    long long v = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
-    if (lane == 31) s_scan[warp] = v;
-    if (lane < C::DEPTH) mbar_init(bar + lane, 1);
-    __syncthreads();
-    long long before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < C::WARPS; ++w) {
-      if (w < warp) before += s_scan[w];
-      all += s_scan[w];
-    }
-    s_pre[tid] = before + v - mine;
-    if (tid == 0) s_pre[32 * C::WARPS] = all;
-    total = all;
-    if (flag && blockIdx.x == 0) set_status(p.status, SPEC_DEV_BAD_LEN);
-    __syncthreads();
-  }
+  if (lane < C::DEPTH) mbar_init(bar + lane, 1);
+  const long long total = attn_prefix<C::ROWS, AT_UNIT, 32 * C::WARPS>(p, s_pre, s_scan, [] { __syncthreads(); });
+  __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
   const int workers = gridDim.x * C::WARPS, me = warp * gridDim.x + blockIdx.x;
   const long long share = (total + workers - 1) / workers;
   const long long begin = me * share;
   const long long end = begin + share < total ? begin + share : total;
-  float* parts = reinterpret_cast<float*>(static_cast<char*>(p.ws) + AT_MAX_CTAS * AT_WARPS * sizeof(AttnSplit));
+  float* parts = attn_parts(p);
   AttnSplit* splits = static_cast<AttnSplit*>(p.ws);
   AttnSplit split{0, -1, 0, 0, 0, 0, 0};
   uint8_t* ring = smem + warp * C::WARP_BYTES;
   uint4* s_q = reinterpret_cast<uint4*>(ring + C::DEPTH * C::UNIT_BYTES);
 
   if (begin < end) {
-    // The segment that holds unit `pos`.
-    auto locate = [&](long long pos) {
-      int lo = 0, hi = 32 * C::WARPS;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_pre[mid] <= pos) lo = mid; else hi = mid;
-      }
-      long long left = pos - s_pre[lo];
-      AttnSeg s;
-      int tiles;
-      for (int b = lo * items;; ++b) {
-        bool outside;
-        const long long w = attn_work<C::ROWS>(p, b, s.n, s.r0, s.L, tiles, s.nu, s.bad, outside);
-        if (left < w) {
-          s.b = b;
-          break;
-        }
-        left -= w;
-      }
-      const long long seg = left / s.nu;
-      s.u = (int)(left - seg * s.nu);
-      s.h = (int)(seg / tiles);
-      s.tile = (int)(seg - (long long)s.h * tiles);
-      return s;
-    };
-    const int bpp = p.P / CACHE_BLOCK;
+    auto locate = [&](long long at) { return attn_locate<C::ROWS, AT_UNIT, 32 * C::WARPS>(p, s_pre, at); };
+    const int bpp = p.P / CACHE_BLOCK, page_bits = 31 - __clz(p.P);
+    const size_t head_bytes = (size_t)bpp * cache_block_bytes(C::D);
 
-    // ---- producer: copies of the units ahead
+    // ---- producer: copies of the units ahead.  `run` units from src on lie in
+    // one page, one segment and this share; the next page's id is read a page
+    // ahead.  A bad page is replaced by page 0 here and found by the consumer.
     AttnSeg ps = locate(begin);
     long long ppos = begin;
-    int issued = 0, consumed = 0, drain = 0;             // units
-    uint32_t bad_stage = 0;
-    bool timed_out = false;
-    auto pages_of = [&](const AttnSeg& s) {              // lane i < 2: page of the unit's block i
-      const int tok = s.u * AT_UNIT + (lane & 1) * CACHE_BLOCK;
-      int page = -1;
-      if (lane < 2 && !s.bad && tok < s.L) page = __ldg(p.table + (size_t)s.b * p.stride + tok / p.P);
-      return page;
+    int istage = 0, run = 0;
+    const bool big = p.P >= AT_UNIT;
+    const uint8_t* src = nullptr;
+    bool second = true;                                  // 16-token pages: the unit has a second one
+    auto page_id = [&](int tok) {                        // of the page that holds token tok of ps (-1: none)
+      return !ps.bad && tok < ps.L ? __ldg(p.table + (size_t)ps.b * p.stride + (tok >> page_bits)) : -1;
     };
-    int page = pages_of(ps);
-    auto issue = [&]() {
-      const int st = issued % C::DEPTH;
+    int next = page_id(ps.u * AT_UNIT + (big ? 0 : (lane & 1) * CACHE_BLOCK));
+    auto refill = [&]() {
+      if (ps.u >= ps.nu) {
+        ps = locate(ppos);
+        next = page_id(ps.u * AT_UNIT + (big ? 0 : (lane & 1) * CACHE_BLOCK));
+      }
       const int tok = ps.u * AT_UNIT;
-      const bool second = tok + CACHE_BLOCK < ps.L;
-      const bool ok_mine = page >= 0 && page < p.num_pages;
-      const uint32_t okm = __ballot_sync(0xffffffffu, ok_mine);
-      const bool ok = !ps.bad && (okm & 1u) && (!second || (okm & 2u));
-      if (!ok) {
-        bad_stage |= 1u << st;
-        if (lane == 0) {
-          if (!ps.bad) set_status(p.status, SPEC_DEV_BAD_SLOT);
-          mbar_arrive1(bar + st);
-        }
+      const int page = next >= 0 && next < p.num_pages ? next : 0;
+      src = p.cache + ((size_t)page * p.Hkv + ps.h) * head_bytes;
+      if (big) {
+        const int in_page = (tok & (p.P - 1)) / AT_UNIT, left = p.P / AT_UNIT - in_page;
+        src += (size_t)in_page * C::UNIT_BYTES;
+        run = min(min(left, ps.nu - ps.u), end - ppos < left ? (int)(end - ppos) : left);
+        next = page_id(tok + left * AT_UNIT);
       } else {
-        bad_stage &= ~(1u << st);
-        uint8_t* dst = ring + st * C::UNIT_BYTES;
-        const int blk = (tok % p.P) / CACHE_BLOCK;
-        if (p.P >= AT_UNIT) {
-          if (lane == 0) {
-            expect_bytes(bar + st, C::UNIT_BYTES);
-            bulk_load(dst, p.cache + cache_block_at(page, ps.h, blk, p.Hkv, bpp, C::D), C::UNIT_BYTES, bar + st);
-          }
-        } else {
-          if (lane == 0) expect_bytes(bar + st, second ? C::UNIT_BYTES : C::UNIT_BYTES / 2);
-          __syncwarp();
-          if (lane == 0 || (lane == 1 && second))
-            bulk_load(dst + lane * (C::UNIT_BYTES / 2), p.cache + cache_block_at(page, ps.h, 0, p.Hkv, bpp, C::D),
-                      C::UNIT_BYTES / 2, bar + st);
-        }
-      }
-      ++issued;
-      ++ppos;
-      if (ppos < end) {
-        if (++ps.u >= ps.nu) ps = locate(ppos);
-        page = pages_of(ps);
+        run = 1;
+        second = tok + CACHE_BLOCK < ps.L;
+        next = page_id(tok + AT_UNIT + (lane & 1) * CACHE_BLOCK);
       }
     };
-    while (issued < C::DEPTH && ppos < end) issue();
+    auto issue = [&]() {
+      if (run == 0) refill();
+      uint64_t* ibar = bar + istage;
+      uint8_t* dst = ring + istage * C::UNIT_BYTES;
+      if (big) {
+        if (lane == 0) {
+          expect_bytes(ibar, C::UNIT_BYTES);
+          bulk_load(dst, src, C::UNIT_BYTES, ibar);
+        }
+        src += C::UNIT_BYTES;
+      } else {
+        if (lane == 0) expect_bytes(ibar, second ? C::UNIT_BYTES : C::UNIT_BYTES / 2);
+        __syncwarp();
+        if (lane == 0 || (lane == 1 && second))
+          bulk_load(dst + lane * (C::UNIT_BYTES / 2), src, C::UNIT_BYTES / 2, ibar);
+      }
+      if (++istage == C::DEPTH) istage = 0;
+      --run;
+      ++ps.u;
+      ++ppos;
+    };
+    for (int i = 0; i < C::DEPTH && ppos < end; ++i) issue();
+    int cstage = 0;
+    uint32_t cphase = 0;
+    bool timed_out = false;
 
     long long pos = begin;
-    while (pos < end) {
-      AttnSeg sg = locate(pos);
+    while (pos < end && !timed_out) {
+      const AttnSeg sg = locate(pos);
       const int u_first = sg.u;
       const int u_end = sg.nu - sg.u < end - pos ? sg.nu : sg.u + (int)(end - pos);
       const int rows = sg.n * p.G, ctx = sg.L - sg.n;
@@ -423,32 +253,31 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
         for (int j = 0; j < C::NV; ++j)
 #pragma unroll
           for (int k = 0; k < 4; ++k) O[m][j][k] = 0.f;
-      bool poison = false;
+      bool poison = sg.bad;                              // a page outside the cache in this part
+      if (!sg.bad) {
+        const int tok_end = min(sg.L, u_end * AT_UNIT);
+        bool bad = false;
+        for (int pg = (u_first * AT_UNIT >> page_bits) + lane; pg << page_bits < tok_end; pg += 32) {
+          const int id = __ldg(p.table + (size_t)sg.b * p.stride + pg);
+          bad |= id < 0 || id >= p.num_pages;
+        }
+        poison = __any_sync(0xffffffffu, bad);
+        if (poison && lane == 0) set_status(p.status, SPEC_DEV_BAD_SLOT);
+      }
+      const bool upper = C::M > 1 || rows - sg.tile * C::ROWS > 8;   // rows 8.. of the tile exist
 
       for (int u = u_first; u < u_end; ++u) {
-        const int st = consumed % C::DEPTH;
-        if (!timed_out && !mbar_wait(bar + st, (uint32_t)(consumed / C::DEPTH) & 1u, 1u << 22)) {
-          timed_out = true;
-          drain = consumed;
+        if (!bar_wait(bar + cstage, cphase)) timed_out = true;
+        timed_out = __any_sync(0xffffffffu, timed_out);
+        if (timed_out) {
           if (lane == 0) set_status(p.status, SPEC_DEV_TIMEOUT);
-        }
-        if (__any_sync(0xffffffffu, timed_out) && !timed_out) {
-          timed_out = true;
-          drain = consumed;
-        }
-        const bool skip = ((bad_stage >> st) & 1u) || timed_out;
-        if (skip) {
           poison = true;
-        } else {
-          const uint8_t* unit = ring + st * C::UNIT_BYTES;
+          break;
+        }
+        {
+          const uint8_t* unit = ring + cstage * C::UNIT_BYTES;
           // ---- first product: scores of 4 x 8 tokens
           float S[C::M][4][4];
-#pragma unroll
-          for (int m = 0; m < C::M; ++m)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) S[m][j][k] = 0.f;
           uint32_t kc[4][C::KW], ks[4][C::KG];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -492,13 +321,25 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
 #pragma unroll
               for (int term = 0; term < C::NT; ++term)
 #pragma unroll
-                for (int m = 0; m < C::M; ++m) mma_f16(S[m][j], a[term][m], b0, b1);
+                for (int m = 0; m < C::M; ++m) {
+                  if (s == 0 && term == 0) mma_f16_first(S[m][j], a[term][m], b0, b1);
+                  else mma_f16(S[m][j], a[term][m], b0, b1);
+                }
             }
           }
           // ---- masks, where the unit reaches the new tokens
           const int tok0 = u * AT_UNIT;
           const bool edge = tok0 + AT_UNIT > ctx;
           if (edge) {
+            // bytes that nobody wrote: V scales of 0 (the last read of K's is above)
+            const int t0 = tok0 + lane;
+            if (t0 >= sg.L) {
+              uint8_t* sc = const_cast<uint8_t*>(unit) + (lane >> 4) * (18 * C::D) + cache_v_scales(C::D) + (lane & 15) * (C::D / 16);
+#pragma unroll
+              for (int i = 0; i < C::D / 64; ++i) reinterpret_cast<uint32_t*>(sc)[i] = 0;
+            }
+            fence_async_shared();                        // before the stage's next copy
+            __syncwarp();
 #pragma unroll
             for (int i = 0; i < 2 * C::M; ++i)
 #pragma unroll
@@ -525,7 +366,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
             const int m = i >> 1, e = 2 * (i & 1);
             float x = fmaxf(S[m][0][e], S[m][0][e + 1]);
 #pragma unroll
-            for (int j = 1; j < 4; ++j) x = fmaxf(x, fmaxf(S[m][j][e], S[m][j][e + 1]));
+            for (int j = 1; j < 4; ++j) x = max3(x, S[m][j][e], S[m][j][e + 1]);
             top[i] = x;
             far |= c[i] * (x - mref[i]) > AT_SLACK;
           }
@@ -551,6 +392,11 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
 #pragma unroll
           for (int i = 0; i < 2 * C::M; ++i) {
             const int m = i >> 1, e = 2 * (i & 1);
+            if (i == 1 && !upper) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) S[m][j][e] = S[m][j][e + 1] = 0.f;
+              continue;
+            }
             const float base = mref[i] == -INFINITY ? 0.f : AT_SHIFT - c[i] * mref[i];
             float sum = 0.f;
 #pragma unroll
@@ -588,35 +434,44 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const uint8_t* blk = unit + k * (18 * C::D);
-            uint32_t vc[4][C::VW], vs[4][2];
+            // tokens t and t + 4 in one word, t + 8 and t + 12 in the other: the
+            // even elements' codes side by side in `even`, the odd ones' in `odd`
+            uint32_t even[2][C::VW], odd[2][C::VW], vs[2][2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int tok = t + 4 * i;
-              const uint8_t* row = blk + cache_v_codes(C::D) + tok * (C::D / 2) + g * (C::D / 16);
-              if (C::D == 64) {
-                vc[i][0] = *reinterpret_cast<const uint32_t*>(row);
-              } else if (C::D == 128) {
-                const uint2 v = *reinterpret_cast<const uint2*>(row);
-                vc[i][0] = v.x; vc[i][C::VW - 1] = v.y;
-              } else {
-                const uint4 v = *reinterpret_cast<const uint4*>(row);
-                vc[i][0] = v.x; vc[i][1 % C::VW] = v.y; vc[i][2 % C::VW] = v.z; vc[i][3 % C::VW] = v.w;
+            for (int i = 0; i < 2; ++i) {
+              uint32_t a[C::VW], b[C::VW], sa, sb;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int tok = t + 8 * i + 4 * e;
+                const uint8_t* row = blk + cache_v_codes(C::D) + tok * (C::D / 2) + g * (C::D / 16);
+                uint32_t* w = e ? b : a;
+                if (C::D == 64) {
+                  w[0] = *reinterpret_cast<const uint32_t*>(row);
+                } else if (C::D == 128) {
+                  const uint2 v = *reinterpret_cast<const uint2*>(row);
+                  w[0] = v.x; w[C::VW - 1] = v.y;
+                } else {
+                  const uint4 v = *reinterpret_cast<const uint4*>(row);
+                  w[0] = v.x; w[1 % C::VW] = v.y; w[2 % C::VW] = v.z; w[3 % C::VW] = v.w;
+                }
+                const uint8_t* sc = blk + cache_v_scales(C::D) + tok * (C::D / 16);
+                uint32_t two = C::D == 256 ? *reinterpret_cast<const uint16_t*>(sc + 2 * g)
+                                           : (uint32_t)sc[C::D == 128 ? g : g >> 1];
+                if (e) sb = two; else sa = two;
               }
-              const uint8_t* sc = blk + cache_v_scales(C::D) + tok * (C::D / 16);
-              uint32_t two = C::D == 256 ? *reinterpret_cast<const uint16_t*>(sc + 2 * g)
-                                         : (uint32_t)sc[C::D == 128 ? g : g >> 1];
-              if (edge && tok0 + 16 * k + tok >= sg.L) two = 0;   // bytes that nobody wrote
-              two = decode_scales(two);
-              vs[i][0] = __byte_perm(two, two, 0x1010);
-              vs[i][1] = C::D == 256 ? __byte_perm(two, two, 0x3232) : vs[i][0];
+              vs[i][0] = decode_scales(__byte_perm(sa, sb, 0x0040));
+              vs[i][1] = C::D == 256 ? decode_scales(__byte_perm(sa, sb, 0x0051)) : vs[i][0];
+#pragma unroll
+              for (int w = 0; w < C::VW; ++w) {
+                even[i][w] = (a[w] & 0x0f0f0f0fu) | ((b[w] << 4) & 0xf0f0f0f0u);
+                odd[i][w] = ((a[w] >> 4) & 0x0f0f0f0fu) | (b[w] & 0xf0f0f0f0u);
+              }
             }
 #pragma unroll
             for (int jj = 0; jj < C::NV / 2; ++jj) {
-              uint32_t v[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) v[i] = mul_h2(decode_byte(vc[i], jj), vs[i][C::D == 256 ? jj >> 3 : 0]);
-              const uint32_t b0 = __byte_perm(v[0], v[1], 0x5410), b1 = __byte_perm(v[2], v[3], 0x5410);
-              const uint32_t d0 = __byte_perm(v[0], v[1], 0x7632), d1 = __byte_perm(v[2], v[3], 0x7632);
+              const int sg2 = C::D == 256 ? jj >> 3 : 0;
+              const uint32_t b0 = mul_h2(decode_byte(even[0], jj), vs[0][sg2]), b1 = mul_h2(decode_byte(even[1], jj), vs[1][sg2]);
+              const uint32_t d0 = mul_h2(decode_byte(odd[0], jj), vs[0][sg2]), d1 = mul_h2(decode_byte(odd[1], jj), vs[1][sg2]);
 #pragma unroll
               for (int term = 0; term < C::NT; ++term)
 #pragma unroll
@@ -627,9 +482,12 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
             }
           }
         }
-        ++consumed;
+        if (++cstage == C::DEPTH) {
+          cstage = 0;
+          cphase ^= 1u;
+        }
         __syncwarp();                                    // all lanes have read the stage
-        if (ppos < end && !timed_out) issue();
+        if (ppos < end) issue();
       }
 
       // ---- the segment's end in this share
@@ -675,7 +533,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
           for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int j = 0; j < C::NV; j += 4)
-              *reinterpret_cast<float4*>(part + (((i * 2 + k) * (C::NV / 4) + j / 4) * 32 + lane) * 4) =
+              *reinterpret_cast<float4*>(part + rl * C::D + (2 * t + k) * C::NV + j) =
                   make_float4(O[m][j][e + k], O[m][j + 1][e + k], O[m][j + 2][e + k], O[m][j + 3][e + k]);
           if (t == 0)
             *reinterpret_cast<float2*>(part + C::ROWS * C::D + 2 * rl) =
@@ -689,60 +547,15 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
       pos += u_end - u_first;
     }
     if (timed_out)                                       // leave no copy in flight
-      for (int i = drain; i < issued; ++i) mbar_wait(bar + i % C::DEPTH, (uint32_t)(i / C::DEPTH) & 1u, 1u << 22);
+      for (int i = 0; i < C::DEPTH; ++i) {
+        bar_wait(bar + cstage, cphase);
+        if (++cstage == C::DEPTH) {
+          cstage = 0;
+          cphase ^= 1u;
+        }
+      }
   }
   if (lane == 0) splits[me] = split;
-}
-
-// Adds the parts of one split segment: CTA (x, y) takes the segments that begin
-// in warps x, x + gridDim.x, ..; y is one of 2 M groups of eight rows.
-constexpr int JOIN_THREADS = 256;
-template <class C, class DT>
-__global__ void __launch_bounds__(JOIN_THREADS) cache_attention_join_kernel(const __grid_constant__ AttnParams p, int workers) {
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const float* parts = reinterpret_cast<const float*>(static_cast<char*>(p.ws) + AT_MAX_CTAS * AT_WARPS * sizeof(AttnSplit));
-  const AttnSplit* splits = static_cast<const AttnSplit*>(p.ws);
-  const int i = blockIdx.y, tid = threadIdx.x;
-  constexpr int ITEMS = 2 * C::D;                        // float4 of eight rows
-  for (int w = blockIdx.x; w < workers; w += gridDim.x) {
-    const AttnSplit s = splits[w];
-    if (s.last < s.first) continue;
-    const int rows = s.n * p.G;
-    if (s.tile * C::ROWS + 8 * i >= rows) continue;      // uniform over the CTA
-    auto part_of = [&](int x) { return parts + (size_t)(2 * x + (x == s.first ? 1 : 0)) * C::PART; };
-    for (int it = tid; it < ITEMS; it += JOIN_THREADS) {
-      const int lane = it & 31, q = it >> 5;             // q: k * (NV / 4) + j / 4
-      const int g = lane >> 2, t = lane & 3;
-      const int r = s.tile * C::ROWS + 8 * i + g;
-      if (r >= rows) continue;
-      const int ml = C::ROWS * C::D + 2 * (8 * i + g);
-      float m = -INFINITY, sum = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int x = s.first; x <= s.last; ++x) {
-        const float* part = part_of(x);
-        const float2 v = __ldg(reinterpret_cast<const float2*>(part + ml));
-        const float4 o = __ldg(reinterpret_cast<const float4*>(part + ((i * 2 * (C::NV / 4) + q) * 32 + lane) * 4));
-        const float mn = fmaxf(m, v.x);
-        const float ref = mn == -INFINITY ? 0.f : mn;
-        const float fa = exp2f(m - ref), fb = exp2f(v.x - ref);
-        m = mn;
-        sum = sum * fa + v.y * fb;
-        acc.x = acc.x * fa + o.x * fb;
-        acc.y = acc.y * fa + o.y * fb;
-        acc.z = acc.z * fa + o.z * fb;
-        acc.w = acc.w * fa + o.w * fb;
-      }
-      const int tok = r / p.G, hq = s.h * p.G + r - tok * p.G;
-      const size_t at = (size_t)(s.r0 + tok) * p.Hq + hq;
-      const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
-      const int k = q / (C::NV / 4), j = 4 * (q - k * (C::NV / 4));
-      const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-      store4(static_cast<DT*>(p.out) + at * C::D + (2 * t + k) * C::NV + j, x);
-      if (q == 0 && t == 0 && p.lse)
-        p.lse[at] = sum == 0.f ? -INFINITY : 0.69314718056f * (m + log2f(sum));
-    }
-  }
 }
 
 namespace {
@@ -759,17 +572,7 @@ cudaError_t launch_cfg(const AttnParams& p, int sms, cudaStream_t st) {
   if (ctas > units) ctas = units;
   cache_attention_kernel<C, DT><<<(int)ctas, 32 * C::WARPS, C::SMEM, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  const int workers = (int)ctas * C::WARPS;
-  cfg.gridDim = dim3(workers < 2 * sms ? workers : 2 * sms, 2 * C::M);
-  cfg.blockDim = dim3(JOIN_THREADS);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_attention_join_kernel<C, DT>, p, workers);
+  return launch_attention_join<C::D, C::ROWS, DT>(p, (int)ctas * C::WARPS, sms, st);
 }
 }  // namespace
 
@@ -791,10 +594,14 @@ cudaError_t launch_cache_attention(const spec_cache_attention_args& a, int sms, 
     if (a.D == 128) return launch_cfg<AttnCfg<128, 1, 2>, float>(p, sms, st);
     return launch_cfg<AttnCfg<256, 1, 2>, float>(p, sms, st);
   }
-  // 16-row tiles where the mean request has no more rows than that
-  const bool few = (long long)a.T * G <= 16LL * a.B;
-  if (a.D == 64) return few ? launch_cfg<AttnCfg<64, 1, 1>, bf16>(p, sms, st) : launch_cfg<AttnCfg<64, 2, 1>, bf16>(p, sms, st);
-  if (a.D == 128) return few ? launch_cfg<AttnCfg<128, 1, 1>, bf16>(p, sms, st) : launch_cfg<AttnCfg<128, 2, 1>, bf16>(p, sms, st);
+  // 16-row tiles (12 warps of 168 registers), but 32-row tiles (8 warps of 255)
+  // where the mean request nearly fills one: 4 x 90k tokens take 237 us in two
+  // 16-row tiles and 199 us in one of 32; with 8 to 32 rows a request (mean 20)
+  // 128 x 4k tokens take 290 and 305 us, with 100 rows 32 x 2k 267 and 290 us.
+  const long long rows = (long long)a.T * G;
+  const bool wide = rows > 24LL * a.B && rows <= 32LL * a.B;
+  if (a.D == 64) return wide ? launch_cfg<AttnCfg<64, 2, 1>, bf16>(p, sms, st) : launch_cfg<AttnCfg<64, 1, 1>, bf16>(p, sms, st);
+  if (a.D == 128) return wide ? launch_cfg<AttnCfg<128, 2, 1>, bf16>(p, sms, st) : launch_cfg<AttnCfg<128, 1, 1>, bf16>(p, sms, st);
   return launch_cfg<AttnCfg<256, 1, 1>, bf16>(p, sms, st);
 }
 

@@ -30,12 +30,12 @@ def torch():
     return t
 
 
-def check(torch, p, scale=None, **kw):
+def check(torch, p, scale=None, floor=0.0, **kw):
     scale = 1.0 / np.sqrt(p.D) if scale is None else scale
     out, lse, st = p.run(torch, scale, **kw)
     want, wlse, tol_o, tol_l = p.oracle(scale)
     assert st == 0
-    bad = ~(np.abs(out - want) <= tol_o)
+    bad = ~(np.abs(out - want) <= tol_o + floor)
     assert not bad.any(), (np.argwhere(bad)[:5], out[bad][:5], want[bad][:5], tol_o[bad][:5])
     if lse is not None:
         inf = np.isneginf(wlse)
@@ -269,3 +269,82 @@ def test_nan_query_stays_in_its_row(torch):
     keep = np.ones(out.shape[:2], bool)
     keep[1, 2] = False
     assert (np.abs(out - want) <= tol)[keep].all()
+
+
+# heads of 128 elements with more rows than one tile, and with rows that fill a wide tile
+@pytest.mark.parametrize("Hq,Hkv,n", [(8, 2, 5), (8, 1, 4), (4, 1, 8), (6, 2, 7), (32, 8, 8), (16, 2, 9), (24, 1, 3)])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_wide_row_tiles(torch, Hq, Hkv, n, page):
+    rng = np.random.default_rng(Hq * n + page)
+    lens = [n, n + 1, 127, 128, 129, 255, 300, 1000]
+    check(torch, H.Paged(rng, lens, [n] * 8, Hq, Hkv, 128, page, "bf16"))
+
+
+@pytest.mark.parametrize("n", [9, 25, 40, 70])
+@pytest.mark.parametrize("empty", [False, True])
+def test_wide_tree_masks(torch, n, empty):
+    rng = np.random.default_rng(n)
+    p = H.Paged(rng, [n, n + 1, n + 100, n + 500, n + 128], [n] * 5, 4, 1, 128, 32, "bf16", tree=H.tree_of(empty=empty))
+    out, lse = check(torch, p)
+    assert not empty or ((out[n // 2] == 0).all() and np.isneginf(lse[n // 2]).all())
+
+
+def test_wide_ragged_rows_and_long_lengths(torch):
+    rng = np.random.default_rng(31)
+    lens = [20000, 5, 300, 1, 2500, 640, 77]
+    check(torch, H.Paged(rng, lens, [8, 2, 0, 1, 17, 3, 40], 8, 2, 128, 64, "bf16"))
+
+
+def test_wide_large_scores(torch):
+    """A 16-bit float ends at 2^-24: with the row's largest p at 2^7 or more, p below 2^-21 of it
+    are off by up to 2^-32 of it, which shows in an element to which the largest p add zeros."""
+    rng = np.random.default_rng(32)
+    p = H.Paged(rng, [900, 300], [6, 3], 8, 1, 128, 64, "bf16", q_size=8.0)
+    for i, t in enumerate(range(0, 900, 16)):
+        blk = p.cache[p.table[0, t // 64], :, t % 64 // 16]
+        blk[:, 8 * 128:9 * 128] = 0x28 + min(i, 0x55)
+    floor = 2.0 ** -32 * 900 * 6 * 2.0 ** 6 * p.v_scale      # of the tokens' sum of |v|
+    for scale in (0.2, -0.2, 0.0):
+        check(torch, p, scale=scale, floor=floor)
+
+
+def test_wide_query_strides_and_padding_rows(torch):
+    rng = np.random.default_rng(35)
+    p = H.Paged(rng, [900, 300], [6, 3], 8, 1, 128, 64, "bf16")
+    wide = torch.randn((p.T + 4, 10, 128), device="cuda").to(torch.bfloat16)
+    wide[2:2 + p.T, 1:9] = H.dev(p.q, torch.bfloat16)
+    out, lse, st = p.run(torch, 0.1, q=wide[:, 1:9], row_ptr=H.dev(p.ptr + 2))
+    want, _, tol, _ = p.oracle(0.1)
+    assert st == 0 and (np.abs(out[2:11] - want) <= tol).all()
+    assert (out[:2] == 7).all() and (out[11:] == 7).all() and (lse[11:] == 7).all()
+
+
+def test_wide_bad_requests(torch):
+    rng = np.random.default_rng(33)
+    p = H.Paged(rng, [400, 500, 600, 700, 300], [5] * 5, 8, 2, 128, 64, "bf16")
+    want, _, tol, _ = p.oracle(0.1)
+    p.lens[1] = 1
+    p.table[2, 1] = -5
+    p.lens[0] = 64 * p.table.shape[1] + 1
+    out, lse, st = p.run(torch, 0.1)
+    assert st == BAD_LEN | BAD_SLOT
+    assert np.isnan(out[:15]).all() and np.isnan(lse[:15]).all()
+    assert (np.abs(out[15:] - want[15:]) <= tol[15:]).all()
+
+
+def test_wide_nan_query_and_repeats(torch):
+    rng = np.random.default_rng(34)
+    p = H.Paged(rng, rng.integers(100, 3000, 12), [6] * 12, 8, 2, 128, 16, "bf16")
+    want, _, tol, _ = p.oracle(0.1)
+    a = p.run(torch, 0.1)
+    for _ in range(3):
+        b = p.run(torch, 0.1, stream=torch.cuda.Stream())
+        np.testing.assert_array_equal(a[0], b[0])
+        np.testing.assert_array_equal(a[1], b[1])
+    q = p.q.copy()
+    q[7, 3, 9], q[20, 0, 100] = np.nan, np.inf
+    out, lse, _ = p.run(torch, 0.1, q=H.dev(q, torch.bfloat16))
+    bad = np.zeros(out.shape[:2], bool)
+    bad[7, 3] = bad[20, 0] = True
+    assert np.isnan(out[bad]).all()
+    assert (np.abs(out - want) <= tol)[~bad].all()
