@@ -8,9 +8,9 @@
 // 256 threads x 8 vectors of 16 bytes, all requested at once and kept in
 // registers, so that maximum, sums and candidates come from one load.
 //
-// The K largest: a thread's maximum is at hand, so the K-th largest of 32
-// group maxima (8 threads each) is a bound that at least K entries reach and,
-// for values in no particular order, some 30 to 130 of 16384 do.  Those are
+// The K largest: a thread's maximum is at hand, so the K-th largest of 64
+// group maxima (4 threads each) is a bound that at least K entries reach and,
+// for values in no particular order, some 10 to 50 of 16384 do.  Those are
 // collected and ranked by counting.  Equal values beyond the list's size (a
 // row of few different values) are found one by one instead.
 //
@@ -23,6 +23,7 @@ namespace spec {
 
 struct LogprobParams {
   int B, n, V, K, segments;
+  float inv_n;                            // 1 / n: row / n without a division
   const void* logits;
   long long b_stride, row_stride;
   const int* tokens;
@@ -36,7 +37,7 @@ struct LogprobParams {
   unsigned long long* keys;               // [rows][segments][K], descending
 };
 
-constexpr int LP_THREADS = 256, LP_WARPS = LP_THREADS / 32, LP_VECS = 8, LP_GROUPS = 32, LP_LIST = 256;
+constexpr int LP_THREADS = 256, LP_WARPS = LP_THREADS / 32, LP_VECS = 8, LP_GROUPS = 64, LP_LIST = 256;
 constexpr float LP_LN2 = 0.69314718056f;
 
 template <class DT>
@@ -85,14 +86,51 @@ __device__ __forceinline__ float vec_get(const uint4& v, int e, const float*) {
 }
 __device__ __forceinline__ uint32_t neg_inf_word(const bf16*) { return 0xff80ff80u; }
 __device__ __forceinline__ uint32_t neg_inf_word(const float*) { return 0xff800000u; }
-__device__ __forceinline__ void vec_set(uint4& v, int e, bf16 x) {
-  const uint32_t b = *reinterpret_cast<const uint16_t*>(&x);
-  uint32_t& w = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
-  w = e & 1 ? (w & 0xffffu) | b << 16 : (w & 0xffff0000u) | b;
+// A value below every entry that counts, finite so that 0 times its distance is 0.
+__device__ __forceinline__ uint32_t low_word(const bf16*) { return 0xf14af14au; }     // -1e30
+__device__ __forceinline__ uint32_t low_word(const float*) { return 0xf149f2cau; }
+// Bits of an element.
+__device__ __forceinline__ uint32_t bits_of(bf16 x) { return *reinterpret_cast<const uint16_t*>(&x); }
+__device__ __forceinline__ uint32_t bits_of(float x) { return __float_as_uint(x); }
+// The vector of elements [at, at + E) of a row of V, -inf where there is none.
+template <class DT>
+__device__ __noinline__ uint4 edge_vector(const DT* x, int at, int V) {
+  constexpr int E = 16 / sizeof(DT), PER = 4 / sizeof(DT);
+  const uint32_t w = neg_inf_word(static_cast<const DT*>(nullptr));
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[i] = w;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int v = at + i * PER + e;
+      if (v >= 0 && v < V) o[i] = PER == 1 ? bits_of(x[v]) : e ? (o[i] & 0xffffu) | bits_of(x[v]) << 16 : (o[i] & 0xffff0000u) | bits_of(x[v]);
+    }
+  }
+  (void)E;
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
-__device__ __forceinline__ void vec_set(uint4& v, int e, float x) {
-  uint32_t& w = e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w;
-  w = __float_as_uint(x);
+// Two fp32 numbers in one operand; additions and products of both in one
+// instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -118,9 +156,11 @@ __device__ __forceinline__ void write_nothing(const LogprobParams& p, int row, i
     p.top_lp[(size_t)row * p.K + k] = quiet_nan();
   }
 }
+// Request of a row: rows < 2^20, so the product is off by less than 0.125 / n.
+__device__ __forceinline__ int request_of(const LogprobParams& p, int row) { return (int)(((float)row + 0.5f) * p.inv_n); }
 template <class DT>
 __device__ __forceinline__ const DT* row_at(const LogprobParams& p, int row) {
-  const int b = row / p.n;
+  const int b = request_of(p, row);
   return static_cast<const DT*>(p.logits) + b * p.b_stride + (row - b * p.n) * p.row_stride;
 }
 
@@ -128,16 +168,16 @@ template <class DT>
 __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const __grid_constant__ LogprobParams p) {
   constexpr int E = LpVec<DT>::E, SEG = LpVec<DT>::SEG;
   const DT* const tag = nullptr;
-  __shared__ float s_group[LP_GROUPS];
+  __shared__ __align__(16) float s_group[LP_GROUPS];
   __shared__ float4 s_warp[LP_WARPS];
   __shared__ unsigned long long s_list[LP_LIST];
-  __shared__ float s_bound;
+  __shared__ uint32_t s_bound;
   __shared__ int s_count;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  const int row = blockIdx.x / p.segments, seg = blockIdx.x - row * p.segments;
+  const int row = blockIdx.x, seg = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int token = __ldg(p.tokens + row);
-  const float T = p.temperature ? __ldg(p.temperature + row / p.n) : 1.f;
+  const float T = p.temperature ? __ldg(p.temperature + request_of(p, row)) : 1.f;
   const uint32_t flag = row_flag(p, token, T);
   if (flag) {
     if (p.segments == 1) write_nothing(p, row, tid, LP_THREADS, flag);
@@ -148,53 +188,79 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const __grid_co
   const int lead = (int)(((uintptr_t)x & 15) / sizeof(DT));
   const int i0 = seg * (SEG / E) + tid;
   uint4 v[LP_VECS];
+  float vm[LP_VECS], tm;
+  int edge = -1;                                             // this thread's vector that the row fills in part
 #pragma unroll
   for (int j = 0; j < LP_VECS; ++j) {
     const int at = (i0 + j * LP_THREADS) * E - lead;
-    if (at >= 0 && at + E <= p.V) {
-      v[j] = __ldcs(reinterpret_cast<const uint4*>(x + at));
-    } else {
-      const uint32_t w = neg_inf_word(tag);
-      v[j] = make_uint4(w, w, w, w);
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (at + e >= 0 && at + e < p.V) vec_set(v[j], e, x[at + e]);
-    }
+    const uint32_t w = low_word(tag);
+    v[j] = make_uint4(w, w, w, w);
+    if (at >= 0 && at + E <= p.V) v[j] = __ldcs(reinterpret_cast<const uint4*>(x + at));
+    else if (at + E > 0 && at < p.V) edge = j;
   }
-  if (tid == 0) s_count = 0;
-  // ---- maxima: vector, thread, group of 8 threads, warp
-  float vm[LP_VECS], tm;
+  if (edge >= 0) {
+    const uint4 q = edge_vector(x, (i0 + edge * LP_THREADS) * E - lead, p.V);
 #pragma unroll
-  for (int j = 0; j < LP_VECS; ++j) vm[j] = vec_max(v[j], tag);
+    for (int j = 0; j < LP_VECS; ++j)
+      if (j == edge) v[j] = q;
+  }
+  if (tid == 0) {
+    s_count = 0;
+    s_bound = 0;
+  }
+  // ---- maxima: vector, thread, group of 8 threads, warp
+#pragma unroll
+  for (int j = 0; j < LP_VECS; ++j) {
+    const int at = (i0 + j * LP_THREADS) * E - lead;
+    vm[j] = at + E > 0 && at < p.V ? vec_max(v[j], tag) : -INFINITY;
+  }
   tm = max_nan(max_nan(max_nan(vm[0], vm[1]), max_nan(vm[2], vm[3])), max_nan(max_nan(vm[4], vm[5]), max_nan(vm[6], vm[7])));
   float gm = tm;
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) gm = max_nan(gm, __shfl_xor_sync(0xffffffffu, gm, o));
-  if ((lane & 7) == 0) s_group[tid >> 3] = gm;
+  for (int o = 1; o < 4; o <<= 1) gm = max_nan(gm, __shfl_xor_sync(0xffffffffu, gm, o));
+  if ((lane & 3) == 0) s_group[tid >> 2] = gm;
   float m = gm;
 #pragma unroll
-  for (int o = 8; o < 32; o <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = 4; o < 32; o <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   // ---- sums against the warp's maximum; an entry of -inf adds nothing
   const float c = 1.4426950408889634f / T;
   const float base = m == -INFINITY ? 0.f : -m * c;
   float z = 0.f, w1 = 0.f;
-  auto sums = [&](auto dist) {
+  {
+    const uint64_t c2 = pair(c, c), b2 = pair(base, base);
+    uint64_t z2[2] = {0, 0}, w2[2] = {0, 0};
 #pragma unroll
+    for (int j = 0; j < LP_VECS; ++j)
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const uint64_t d2 = fma2(pair(vec_get(v[j], e, tag), vec_get(v[j], e + 1, tag)), c2, b2);
+        const float2 d = unpair(d2);
+        const uint64_t y2 = pair(ex2(d.x), ex2(d.y));
+        z2[j & 1] = add2(z2[j & 1], y2);
+        w2[j & 1] = fma2(y2, d2, w2[j & 1]);
+      }
+    const float2 zs = unpair(add2(z2[0], z2[1])), ws = unpair(add2(w2[0], w2[1]));
+    z = zs.x + zs.y;
+    w1 = ws.x + ws.y;
+  }
+  if (__any_sync(0xffffffffu, !(fabsf(w1) <= 3.4e38f))) {
+    // an entry of -inf (0 times its distance), or numbers near the floats' end:
+    // once more, distances first and bounded
+    z = w1 = 0.f;
     for (int j = 0; j < LP_VECS; ++j) {
+      const int at = (i0 + j * LP_THREADS) * E - lead;
       float zz = 0.f, ww = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float d = fmaxf(dist(vec_get(v[j], e, tag)), -200.f);
-        const float y = ex2(d);
-        zz += y;
-        ww = fmaf(y, d, ww);
+      for (int e = max(0, -at); e < E && at + e < p.V; ++e) {
+        const float y = tof(x[at + e]);
+        const float d = y == -INFINITY ? -200.f : fmaxf((y - m) * c, -200.f);
+        const float q = ex2(d);
+        zz += q;
+        ww = fmaf(q, d, ww);
       }
       z += zz;
       w1 += ww;
     }
-  };
-  if (fabsf(base) < 3.0e38f) sums([&](float y) { return fmaf(y, c, base); });
-  else sums([&](float y) { return (y - m) * c; });           // m / T beyond the floats
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     z += __shfl_xor_sync(0xffffffffu, z, o);
@@ -204,38 +270,47 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const __grid_co
   __syncthreads();
   // ---- bound of the candidates: the K-th largest group maximum
   if (p.K > 0) {
-    if (warp == 0) {
-      const float g = s_group[lane];
-      int above = 0;
-#pragma unroll
-      for (int i = 0; i < LP_GROUPS; ++i) {
-        const float h = s_group[i];
-        above += h > g || (h == g && i < lane);
+    // the largest group maximum that K groups reach; with a NaN none may, and
+    // the row has no distribution
+    if (tid < LP_GROUPS) {
+      const float g = s_group[tid];
+      int reach = 0;
+#pragma unroll 4
+      for (int i = 0; i < LP_GROUPS; i += 4) {
+        const float4 h = *reinterpret_cast<const float4*>(s_group + i);
+        reach += (h.x >= g) + (h.y >= g) + (h.z >= g) + (h.w >= g);
       }
-      if (above == p.K - 1) s_bound = g;                     // NaN: the row has no distribution
-      if (lane == 0 && !(s_group[0] == s_group[0])) s_bound = -INFINITY;
+      const uint32_t best = __reduce_max_sync(0xffffffffu, reach >= p.K ? ordered(g) : 0u);
+      if (lane == 0) atomicMax(&s_bound, best);
     }
     __syncthreads();
-    const float bound = s_bound;
-    if (tm >= bound) {
+    const float bound = s_bound ? from_ordered(s_bound) : INFINITY;
+    uint32_t hit = 0;
 #pragma unroll
-      for (int j = 0; j < LP_VECS; ++j)
-        if (vm[j] >= bound) {
-          const int at = (i0 + j * LP_THREADS) * E - lead;
+    for (int j = 0; j < LP_VECS; ++j) hit |= (vm[j] >= bound ? 1u : 0u) << j;
+    // few vectors: read again rather than picked out of the registers, which
+    // would take the code of all eight (it is bound by instruction fetches then)
+    while (hit) {
+      const int j = __ffs(hit) - 1, at = (i0 + j * LP_THREADS) * E - lead;
+      hit &= hit - 1;
+      const uint4 q = at >= 0 && at + E <= p.V ? __ldg(reinterpret_cast<const uint4*>(x + at)) : edge_vector(x, at, p.V);
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float y = vec_get(v[j], e, tag);
-            // entries of -inf count only where the lowest indexes may be needed
-            if (y >= bound && (y > -INFINITY || (at + e >= 0 && at + e < p.V && at + e < seg * SEG - lead + 64))) {
-              const int k = atomicAdd(&s_count, 1);
-              if (k < LP_LIST) s_list[k] = entry_key(y, at + e);
-            }
-          }
+      for (int e = 0; e < E; ++e) {
+        const float y = vec_get(q, e, tag);
+        // entries of -inf count only where the lowest indexes may be needed
+        if (y >= bound && (y > -INFINITY || (at + e >= 0 && at + e < p.V && at + e < seg * SEG - lead + 64))) {
+          const int k = atomicAdd(&s_count, 1);
+          if (k < LP_LIST) s_list[k] = entry_key(y, at + e);
         }
+      }
     }
     __syncthreads();
   }
-  // ---- this segment's part: every thread has it, warp by warp in order
+  // ---- this segment's part, warp by warp in order, and its K largest: the
+  // first warp's work, unless the list overflowed
+  const bool single = p.segments == 1;
+  const int count = p.K > 0 ? s_count : 0;
+  if (warp > 0 && count <= LP_LIST) return;
   float pm = s_warp[0].x;
 #pragma unroll
   for (int i = 1; i < LP_WARPS; ++i) pm = max_nan(pm, s_warp[i].x);
@@ -247,15 +322,16 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const __grid_co
     pz += q.y * f;
     pw += f * fmaf(q.y, d, q.z);
   }
-  const bool single = p.segments == 1;
   const bool bad = !(pm < INFINITY) || (single && pm == -INFINITY);
-  if (!single && tid == 0) p.part[blockIdx.x] = make_float4(pm, pz, pw, 0.f);
-  const float lz = LP_LN2 * log2f(pz);
+  const size_t at_part = (size_t)row * p.segments + seg;
+  if (!single && tid == 0) p.part[at_part] = make_float4(pm, pz, pw, 0.f);
+  float lz = 0.f;
   if (single) {
     if (bad) {
-      write_nothing(p, row, tid, LP_THREADS, SPEC_DEV_BAD_LOGIT);
+      write_nothing(p, row, tid, 32, SPEC_DEV_BAD_LOGIT);
       return;
     }
+    lz = LP_LN2 * log2f(pz);
     if (tid == 0) {
       p.logprob[row] = (tof(x[token]) - pm) / T - lz;
       p.entropy[row] = lz - LP_LN2 * pw / pz;
@@ -267,18 +343,18 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const __grid_co
       p.top_ids[(size_t)row * p.K + rank] = (int)~(uint32_t)key;
       p.top_lp[(size_t)row * p.K + rank] = (from_ordered((uint32_t)(key >> 32)) - pm) / T - lz;
     } else {
-      p.keys[(size_t)blockIdx.x * p.K + rank] = key;
+      p.keys[at_part * p.K + rank] = key;
     }
   };
-  const int count = s_count;
   if (count <= LP_LIST) {
-    if (tid < count) {
-      const unsigned long long mine = s_list[tid];
+    for (int k = lane; k < count; k += 32) {
+      const unsigned long long mine = s_list[k];
       int rank = 0;
+#pragma unroll 4
       for (int i = 0; i < count; ++i) rank += s_list[i] > mine;
       if (rank < p.K) put(rank, mine);
     }
-    if (!single && tid >= count && tid < p.K) put(tid, 0);   // a segment of fewer entries
+    if (!single && lane >= count && lane < p.K) put(lane, 0);   // a segment of fewer entries
   } else {
     // too many equal values: the largest below the last one found, K times
     unsigned long long last = ~0ull;
@@ -310,12 +386,12 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const __grid_co
 constexpr int LPJ_WARPS = 4;
 template <class DT>
 __global__ void __launch_bounds__(32 * LPJ_WARPS) logprobs_join_kernel(const __grid_constant__ LogprobParams p) {
-  extern __shared__ uint8_t s_next[];                        // [warps][segments] candidates taken (multi-pass rows)
+  extern __shared__ unsigned long long s_lists[];            // [warps][33][K]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.x * LPJ_WARPS + warp;
   if (row < p.B * p.n) {
     const int token = __ldg(p.tokens + row);
-    const float T = p.temperature ? __ldg(p.temperature + row / p.n) : 1.f;
+    const float T = p.temperature ? __ldg(p.temperature + request_of(p, row)) : 1.f;
     const uint32_t flag = row_flag(p, token, T);
     const float xt = flag ? 0.f : tof(row_at<DT>(p, row)[token]);
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
@@ -351,35 +427,33 @@ __global__ void __launch_bounds__(32 * LPJ_WARPS) logprobs_join_kernel(const __g
       p.entropy[row] = lz - LP_LN2 * w1 / z;
     }
     if (p.K == 0) return;
-    uint8_t* next = s_next + warp * p.segments;
     const unsigned long long* keys = p.keys + (size_t)row * p.segments * p.K;
-    // the best of this lane's lists and where it is
-    unsigned long long head = 0;
-    int from = -1;
-    auto look = [&]() {
-      head = 0;
-      for (int s = lane; s < p.segments; s += 32) {
-        const int at = next[s];
-        const unsigned long long key = at < p.K ? keys[(size_t)s * p.K + at] : 0;
-        if (key > head) {
-          head = key;
-          from = s;
-        }
-      }
-    };
-    for (int s = lane; s < p.segments; s += 32) next[s] = 0;
-    __syncwarp();
-    look();
     unsigned long long mine = 0;                             // lane k keeps the k-th
-    for (int k = 0; k < p.K; ++k) {
-      const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(head >> 32));
-      const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(head >> 32) == hi ? (uint32_t)head : 0u);
-      const unsigned long long best = (unsigned long long)hi << 32 | lo;
-      if (lane == k) mine = best;
-      if (head == best && best) {
-        ++next[from];
-        look();
+    // 32 segments at a time: their sorted lists and the best so far in shared
+    // memory, and K times the largest of the lists' heads
+    unsigned long long* s_keys = s_lists + warp * (33 * p.K);
+    for (int s0 = 0; s0 < p.segments; s0 += 32) {
+      const int lists = min(32, p.segments - s0);
+      __syncwarp();
+      for (int i = lane; i < lists * p.K; i += 32) s_keys[i] = keys[(size_t)s0 * p.K + i];
+      if (lane < p.K) s_keys[32 * p.K + lane] = mine;        // the best so far
+      __syncwarp();
+      int at = 0, at_best = 0;
+      unsigned long long head = lane < lists ? s_keys[lane * p.K] : 0, kept = s0 ? s_keys[32 * p.K] : 0;
+      unsigned long long out = 0;
+      for (int k = 0; k < p.K; ++k) {
+        const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(head >> 32));
+        const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(head >> 32) == hi ? (uint32_t)head : 0u);
+        unsigned long long best = (unsigned long long)hi << 32 | lo;
+        if (kept > best) {                                   // uniform
+          best = kept;
+          kept = ++at_best < p.K ? s_keys[32 * p.K + at_best] : 0;
+        } else if (head == best && best) {
+          head = ++at < p.K ? s_keys[lane * p.K + at] : 0;
+        }
+        if (lane == k) out = best;
       }
+      mine = out;
     }
     if (lane < p.K) {
       p.top_ids[(size_t)row * p.K + lane] = (int)~(uint32_t)mine;
@@ -411,14 +485,14 @@ static cudaError_t launch(LogprobParams p, const spec_logprobs_args& a, cudaStre
   p.segments = (a.V + (even ? 0 : E - 1) + LpVec<DT>::SEG - 1) / LpVec<DT>::SEG;
   p.part = static_cast<float4*>(a.workspace);
   p.keys = reinterpret_cast<unsigned long long*>(p.part + (size_t)rows * p.segments);
-  if ((long long)rows * p.segments > 0x7fffffff) return cudaErrorInvalidValue;
-  logprobs_kernel<DT><<<rows * p.segments, LP_THREADS, 0, st>>>(p);
+  p.inv_n = 1.f / (float)a.n;
+  logprobs_kernel<DT><<<dim3(rows, p.segments), LP_THREADS, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.segments == 1) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((rows + LPJ_WARPS - 1) / LPJ_WARPS);
   cfg.blockDim = dim3(32 * LPJ_WARPS);
-  cfg.dynamicSmemBytes = (size_t)LPJ_WARPS * p.segments;
+  cfg.dynamicSmemBytes = (size_t)LPJ_WARPS * 33 * p.K * sizeof(unsigned long long);   // at most 33 KB
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -429,7 +503,7 @@ static cudaError_t launch(LogprobParams p, const spec_logprobs_args& a, cudaStre
 }
 
 cudaError_t launch_logprobs(const spec_logprobs_args& a, int sms, cudaStream_t st) {
-  LogprobParams p{a.B, a.n, a.V, a.K, 0, a.logits, a.b_stride, a.row_stride, a.tokens, a.temperature, a.logprob,
+  LogprobParams p{a.B, a.n, a.V, a.K, 0, 0.f, a.logits, a.b_stride, a.row_stride, a.tokens, a.temperature, a.logprob,
                   a.entropy, a.top_ids, a.top_logprobs, a.dev_status, nullptr, nullptr};
   return a.dtype == SPEC_BF16 ? launch<bf16>(p, a, st) : launch<float>(p, a, st);
 }
