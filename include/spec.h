@@ -506,7 +506,8 @@ int32_t spec_block_tables(const spec_block_tables_args* args, spec_stream_t stre
  * zeros for skipped rows.  A slot outside the cache sets SPEC_DEV_BAD_SLOT and
  * its row is skipped; two rows with one slot leave either's token there.
  * k, v: rows of Hkv heads of D elements, row and head strides in elements
- * (multiples of 8 for bf16, of 4 for fp32).  1 <= Hkv <= 256, 0 <= T < 2^24. */
+ * (multiples of 8 for bf16, of 4 for fp32).  1 <= Hkv <= 256, 0 <= T < 2^24,
+ * (T + 16) Hkv D < 2^36.                                                    */
 typedef struct {
   int32_t T, Hkv, D, dtype;
   int32_t page_size, num_pages;

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libspec.so")
@@ -206,17 +207,17 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     L.spec_cache_bytes.restype = _sz
     L.spec_cache_bytes.argtypes = [_i32, _i32, _i32, _i32]
     L.spec_block_tables.restype = _i32
-    L.spec_block_tables.argtypes = [ctypes.POINTER(BlockTablesArgs), _vp]
+    L.spec_block_tables.argtypes = [_vp, _vp]
     L.spec_cache_append.restype = _i32
-    L.spec_cache_append.argtypes = [ctypes.POINTER(CacheAppendArgs), _vp]
+    L.spec_cache_append.argtypes = [_vp, _vp]
     L.spec_cache_attention_workspace_bytes.restype = _sz
     L.spec_cache_attention_workspace_bytes.argtypes = [_i32, _i32, _i32]
     L.spec_cache_attention.restype = _i32
-    L.spec_cache_attention.argtypes = [ctypes.POINTER(CacheAttentionArgs), _vp]
+    L.spec_cache_attention.argtypes = [_vp, _vp]
     L.spec_logprobs_workspace_bytes.restype = _sz
     L.spec_logprobs_workspace_bytes.argtypes = [_i32, _i32, _i32]
     L.spec_logprobs.restype = _i32
-    L.spec_logprobs.argtypes = [ctypes.POINTER(LogprobsArgs), _vp]
+    L.spec_logprobs.argtypes = [_vp, _vp]
     if path is None:
         _LIB = L
     return L
@@ -453,30 +454,72 @@ def spec_tree_verify(target, U, W1, W2, anchor, temperature, parent, mask, token
 
 
 # ------------------------------------------------------- target side of a cycle
+# These calls are made every step of a server, some of them for microseconds of
+# GPU work: their arguments are packed into the C structs' bytes in one go (the
+# formats follow the structures above field by field), and checked by identity
+# and tuple comparison.
 
-def _tensor(t, what: str, dtype: str, shape: tuple) -> int:
+def _format(py) -> struct.Struct:
+    """struct format of a mirror, native alignment."""
+    codes = {_i32: "i", _vp: "P", _i64: "q", _f32: "f", _sz: "N"}
+    return struct.Struct("@" + "".join(codes[t] for _, t in py._fields_) + "0P")
+
+
+_TABLES, _APPEND = _format(BlockTablesArgs), _format(CacheAppendArgs)
+_ATTENTION, _LOGPROBS = _format(CacheAttentionArgs), _format(LogprobsArgs)
+_torch = None
+
+
+def _types():
+    """torch, imported at the first call that needs it."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _raw_stream(stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch._C._cuda_getCurrentRawStream(_torch.cuda.current_device())
+
+
+def _tensor(t, what: str, dtype, shape: tuple) -> int:
     """Address of a contiguous CUDA tensor of this type and shape."""
-    if str(t.dtype) != dtype or tuple(t.shape) != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise SpecError(f"{what} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
-    return _ptr(t)
-
-
-def _heads(t, what: str, T: int, H: int, D: int) -> int:
-    """Address of a CUDA tensor [T][H][D] whose heads are contiguous."""
-    if tuple(t.shape) != (T, H, D) or t.stride(2) != 1:
-        raise SpecError(f"{what} must be [{T}, {H}, {D}] with contiguous heads, not {list(t.shape)} "
-                        f"with strides {list(t.stride())}")
-    if not t.is_cuda:
-        raise SpecError("tensors must be CUDA tensors")
+    if not (t.is_cuda and t.is_contiguous()):
+        raise SpecError(f"{what} must be a contiguous CUDA tensor")
     return t.data_ptr()
+
+
+def _heads(t, what: str, shape: tuple) -> tuple:
+    """Address, row and head stride of a CUDA tensor [T][H][D] whose heads are contiguous."""
+    s = t.stride()
+    if t.shape != shape or s[2] != 1:
+        raise SpecError(f"{what} must be {list(shape)} with contiguous heads, not {list(t.shape)} "
+                        f"with strides {list(s)}")
+    if not t.is_cuda:
+        raise SpecError(f"{what} must be a CUDA tensor")
+    return t.data_ptr(), s[0], s[1]
 
 
 def _cache_shape(cache, D: int) -> tuple:
     """(num_pages, Hkv, page_size) of a 4-bit cache [num_pages][Hkv][page_size / 16][18 D]."""
-    if cache.dim() != 4 or cache.shape[3] != 18 * D or str(cache.dtype) != "torch.uint8":
+    s = cache.shape
+    if len(s) != 4 or s[3] != 18 * D or cache.dtype is not _torch.uint8:
         raise SpecError(f"cache must be torch.uint8 [num_pages, Hkv, page_size / 16, {18 * D}], not "
-                        f"{cache.dtype} {list(cache.shape)}")
-    return cache.shape[0], cache.shape[1], cache.shape[2] * 16
+                        f"{cache.dtype} {list(s)}")
+    return s[0], s[1], s[2] * 16
+
+
+def _storage(t) -> int:
+    if t.dtype is _torch.bfloat16:
+        return SPEC_BF16
+    if t.dtype is _torch.float32:
+        return SPEC_F32
+    raise SpecError(f"unsupported type {t.dtype}")
 
 
 def spec_cache_bytes(num_pages: int, Hkv: int, page_size: int, D: int) -> int:
@@ -488,40 +531,50 @@ def spec_block_tables(seq_len, accept_len, new_len, num_blocks, ring_pos, free_r
                       dev_status, page_size: int, stream=None) -> None:
     """Block tables, slots and positions of every request's next tokens
     (accept_len None: the lengths are final)."""
-    B, i32, i64 = seq_len.shape[0], "torch.int32", "torch.int64"
-    stride, rows = block_table.shape[1], slots.shape[0]
-    a = BlockTablesArgs(
-        B, page_size, free_ring.shape[0], stride, rows, _tensor(seq_len, "seq_len", i32, (B,)),
-        None if accept_len is None else _tensor(accept_len, "accept_len", i32, (B,)),
-        _tensor(new_len, "new_len", i32, (B,)), _tensor(num_blocks, "num_blocks", i32, (B,)),
-        _tensor(ring_pos, "ring_pos", i64, (2,)),
-        _tensor(free_ring, "free_ring", i32, (free_ring.shape[0],)),
-        _tensor(block_table, "block_table", i32, (B, stride)),
-        _tensor(seq_len_out, "seq_len_out", i32, (B,)), _tensor(kv_len, "kv_len", i32, (B,)),
-        _tensor(num_blocks_out, "num_blocks_out", i32, (B,)),
-        _tensor(ring_pos_out, "ring_pos_out", i64, (2,)),
-        _tensor(row_ptr, "row_ptr", i32, (B + 1,)), _tensor(slots, "slots", i32, (rows,)),
-        _tensor(positions, "positions", i32, (rows,)), _tensor(dev_status, "dev_status", i32, (4,)))
-    _check(lib().spec_block_tables(ctypes.byref(a), _stream(stream)), "spec_block_tables")
+    T = _types()
+    i32, i64 = T.int32, T.int64
+    b = tuple(seq_len.shape)
+    B, table, rows, ring = b[0], tuple(block_table.shape), tuple(slots.shape), tuple(free_ring.shape)
+    if len(b) != 1 or len(table) != 2 or len(rows) != 1 or len(ring) != 1 or table[0] != B:
+        raise SpecError("seq_len, slots and free_ring must be vectors, block_table [B, pages]")
+    a = _TABLES.pack(
+        B, page_size, ring[0], table[1], rows[0], _tensor(seq_len, "seq_len", i32, b),
+        0 if accept_len is None else _tensor(accept_len, "accept_len", i32, b),
+        _tensor(new_len, "new_len", i32, b), _tensor(num_blocks, "num_blocks", i32, b),
+        _tensor(ring_pos, "ring_pos", i64, (2,)), _tensor(free_ring, "free_ring", i32, ring),
+        _tensor(block_table, "block_table", i32, table), _tensor(seq_len_out, "seq_len_out", i32, b),
+        _tensor(kv_len, "kv_len", i32, b), _tensor(num_blocks_out, "num_blocks_out", i32, b),
+        _tensor(ring_pos_out, "ring_pos_out", i64, (2,)), _tensor(row_ptr, "row_ptr", i32, (B + 1,)),
+        _tensor(slots, "slots", i32, rows), _tensor(positions, "positions", i32, rows),
+        _tensor(dev_status, "dev_status", i32, (4,)))
+    rc = lib().spec_block_tables(a, _raw_stream(stream))
+    if rc:
+        _check(rc, "spec_block_tables")
 
 
 def spec_cache_append(k, v, slots, cache, dev_status, k_scale: float = 1.0, v_scale: float = 1.0,
                       k_stored=None, v_stored=None, stream=None) -> None:
     """Round keys and values [T][Hkv][D] to 4 bits into the cache at their
     slots; k_stored / v_stored receive the values as stored."""
-    T, H, D = k.shape
+    T = _types()
+    shape = tuple(k.shape)
+    if len(shape) != 3:
+        raise SpecError(f"k must be [T, Hkv, D], not {list(shape)}")
+    rows, H, D = shape
     pages, Hkv, P = _cache_shape(cache, D)
-    dt = str(k.dtype)
-    if Hkv != H or v.dtype != k.dtype:
+    if Hkv != H or v.dtype is not k.dtype:
         raise SpecError(f"k, v and cache disagree: {H} and {Hkv} heads, {k.dtype} and {v.dtype}")
-    a = CacheAppendArgs(
-        T, H, D, _dtype_code(k), P, pages, _heads(k, "k", T, H, D), _heads(v, "v", T, H, D),
-        k.stride(0), k.stride(1), v.stride(0), v.stride(1), _tensor(slots, "slots", "torch.int32", (T,)),
-        k_scale, v_scale, _ptr(cache),
-        None if k_stored is None else _tensor(k_stored, "k_stored", dt, (T, H, D)),
-        None if v_stored is None else _tensor(v_stored, "v_stored", dt, (T, H, D)),
-        _tensor(dev_status, "dev_status", "torch.int32", (4,)))
-    _check(lib().spec_cache_append(ctypes.byref(a), _stream(stream)), "spec_cache_append")
+    kp, kr, kh = _heads(k, "k", shape)
+    vp, vr, vh = _heads(v, "v", shape)
+    a = _APPEND.pack(
+        rows, H, D, _storage(k), P, pages, kp, vp, kr, kh, vr, vh, _tensor(slots, "slots", T.int32, (rows,)),
+        k_scale, v_scale, _tensor(cache, "cache", T.uint8, cache.shape),
+        0 if k_stored is None else _tensor(k_stored, "k_stored", k.dtype, shape),
+        0 if v_stored is None else _tensor(v_stored, "v_stored", k.dtype, shape),
+        _tensor(dev_status, "dev_status", T.int32, (4,)))
+    rc = lib().spec_cache_append(a, _raw_stream(stream))
+    if rc:
+        _check(rc, "spec_cache_append")
 
 
 def spec_cache_attention_workspace_bytes(Hq: int, Hkv: int, D: int) -> int:
@@ -534,21 +587,27 @@ def spec_cache_attention(q, cache, block_table, kv_len, row_ptr, out, dev_status
     """Attention of the packed rows q [T][Hq][D] of every request over its
     cached tokens; tree_mask [T][words] (int32 bit words) replaces the causal
     order among a request's new tokens."""
-    T, Hq, D = q.shape
-    B, stride = block_table.shape
+    T = _types()
+    i32 = T.int32
+    shape, table = tuple(q.shape), tuple(block_table.shape)
+    if len(shape) != 3 or len(table) != 2:
+        raise SpecError(f"q must be [T, Hq, D] and block_table [B, pages], not {list(shape)}, {list(table)}")
+    rows, Hq, D = shape
+    B = table[0]
     pages, Hkv, P = _cache_shape(cache, D)
     words = 0 if tree_mask is None else tree_mask.shape[1]
-    a = CacheAttentionArgs(
-        B, T, Hq, Hkv, D, _dtype_code(q), P, pages, stride, words, _heads(q, "q", T, Hq, D),
-        q.stride(0), q.stride(1), _ptr(cache),
-        _tensor(block_table, "block_table", "torch.int32", (B, stride)),
-        _tensor(kv_len, "kv_len", "torch.int32", (B,)), _tensor(row_ptr, "row_ptr", "torch.int32", (B + 1,)),
-        None if tree_mask is None else _tensor(tree_mask, "tree_mask", "torch.int32", (T, words)),
-        softmax_scale, k_scale, v_scale, _tensor(out, "out", str(q.dtype), (T, Hq, D)),
-        None if lse is None else _tensor(lse, "lse", "torch.float32", (T, Hq)),
-        _tensor(dev_status, "dev_status", "torch.int32", (4,)), _ptr(workspace),
-        workspace.numel() * workspace.element_size())
-    _check(lib().spec_cache_attention(ctypes.byref(a), _stream(stream)), "spec_cache_attention")
+    qp, qr, qh = _heads(q, "q", shape)
+    a = _ATTENTION.pack(
+        B, rows, Hq, Hkv, D, _storage(q), P, pages, table[1], words, qp, qr, qh,
+        _tensor(cache, "cache", T.uint8, cache.shape), _tensor(block_table, "block_table", i32, table),
+        _tensor(kv_len, "kv_len", i32, (B,)), _tensor(row_ptr, "row_ptr", i32, (B + 1,)),
+        0 if tree_mask is None else _tensor(tree_mask, "tree_mask", i32, (rows, words)),
+        softmax_scale, k_scale, v_scale, _tensor(out, "out", q.dtype, shape),
+        0 if lse is None else _tensor(lse, "lse", T.float32, (rows, Hq)),
+        _tensor(dev_status, "dev_status", i32, (4,)), _ptr(workspace), workspace.nbytes)
+    rc = lib().spec_cache_attention(a, _raw_stream(stream))
+    if rc:
+        _check(rc, "spec_cache_attention")
 
 
 def spec_logprobs_workspace_bytes(rows: int, V: int, K: int) -> int:
@@ -559,20 +618,22 @@ def spec_logprobs(logits, tokens, logprob, entropy, dev_status, workspace, tempe
                   top_ids=None, top_logprobs=None, stream=None) -> None:
     """Log probabilities of tokens [B][n] under logits [B][n][V], the entropies,
     and the K = top_ids.shape[2] largest entries of each row."""
-    B, n, V = logits.shape
-    f32, i32 = "torch.float32", "torch.int32"
-    K = 0 if top_ids is None else top_ids.shape[2]
-    if logits.stride(2) != 1 or not logits.is_cuda:
-        raise SpecError("logits must be a CUDA tensor with contiguous rows")
+    T = _types()
+    f32, i32 = T.float32, T.int32
+    shape, s = tuple(logits.shape), logits.stride()
+    if len(shape) != 3 or s[2] != 1 or not logits.is_cuda:
+        raise SpecError("logits must be a CUDA tensor [B, n, V] with contiguous rows")
     if (top_ids is None) != (top_logprobs is None):
         raise SpecError("top_ids and top_logprobs go together")
-    a = LogprobsArgs(
-        B, n, V, K, _dtype_code(logits), logits.data_ptr(), logits.stride(0), logits.stride(1),
-        _tensor(tokens, "tokens", i32, (B, n)),
-        None if temperature is None else _tensor(temperature, "temperature", f32, (B,)),
+    B, n, V = shape
+    K = 0 if top_ids is None else top_ids.shape[2]
+    a = _LOGPROBS.pack(
+        B, n, V, K, _storage(logits), logits.data_ptr(), s[0], s[1], _tensor(tokens, "tokens", i32, (B, n)),
+        0 if temperature is None else _tensor(temperature, "temperature", f32, (B,)),
         _tensor(logprob, "logprob", f32, (B, n)), _tensor(entropy, "entropy", f32, (B, n)),
-        _tensor(top_ids, "top_ids", i32, (B, n, K)) if K else None,
-        _tensor(top_logprobs, "top_logprobs", f32, (B, n, K)) if K else None,
-        _tensor(dev_status, "dev_status", i32, (4,)), _ptr(workspace),
-        workspace.numel() * workspace.element_size())
-    _check(lib().spec_logprobs(ctypes.byref(a), _stream(stream)), "spec_logprobs")
+        _tensor(top_ids, "top_ids", i32, (B, n, K)) if K else 0,
+        _tensor(top_logprobs, "top_logprobs", f32, (B, n, K)) if K else 0,
+        _tensor(dev_status, "dev_status", i32, (4,)), _ptr(workspace), workspace.nbytes)
+    rc = lib().spec_logprobs(a, _raw_stream(stream))
+    if rc:
+        _check(rc, "spec_logprobs")

@@ -806,6 +806,7 @@ int32_t spec_cache_append(const spec_cache_append_args* a, spec_stream_t stream)
     return SPEC_EINVAL;
   if (!page_ok(a->page_size) || !head_ok(a->D) || (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16))
     return SPEC_EUNSUPPORTED;
+  if (((int64_t)a->T + 16) * a->Hkv * a->D >= (int64_t)1 << 36) return SPEC_EINVAL;
   if (a->T == 0) return SPEC_OK;
   if (!a->k || !a->v || !a->slots || !a->cache || !a->dev_status) return SPEC_EINVAL;
   if (!aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(a->slots, 4) || !aligned(a->cache, 16) ||

@@ -31,6 +31,8 @@
 // A segment inside one warp's share is written at once.  Otherwise each part is
 // kept as (m, sum, unnormalised out) in the workspace and
 // cache_attention_join_kernel adds the parts in the order of their warps.
+#include <atomic>
+
 #include "spec_attention.cuh"
 
 namespace spec {
@@ -562,8 +564,16 @@ namespace {
 template <class C, class DT>
 cudaError_t launch_cfg(const AttnParams& p, int sms, cudaStream_t st) {
   static_assert(C::SMEM <= 227 * 1024 - 4096, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(cache_attention_kernel<C, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  // once a device: the attribute stays with the function
+  static std::atomic<uint64_t> sized{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64 || !((sized.load(std::memory_order_relaxed) >> dev) & 1)) {
+    e = cudaFuncSetAttribute(cache_attention_kernel<C, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) sized.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
   // one wave at most, and no more warps than there can be units
   long long ctas = (long long)sms * C::MIN_CTAS;
   if (ctas > C::MIN_CTAS * (AT_MAX_CTAS / 2)) ctas = C::MIN_CTAS * (AT_MAX_CTAS / 2);

@@ -40,6 +40,16 @@ def test_struct_layouts_match_the_header(tmp_path):
         assert int(value) == (ctypes.sizeof(py) if field == "sizeof" else getattr(py, field).offset), line
 
 
+@pytest.mark.parametrize("py,fmt", [(_lib.BlockTablesArgs, _lib._TABLES), (_lib.CacheAppendArgs, _lib._APPEND),
+                                    (_lib.CacheAttentionArgs, _lib._ATTENTION), (_lib.LogprobsArgs, _lib._LOGPROBS)])
+def test_packed_arguments_have_the_structs_layout(py, fmt):
+    values = [i + 1 for i in range(len(py._fields_))]
+    packed = fmt.pack(*values)
+    assert len(packed) == ctypes.sizeof(py)
+    a = py.from_buffer_copy(packed)
+    assert [getattr(a, f) for f, _ in py._fields_] == values
+
+
 def make(py, **kw):
     """Arguments whose pointers are distinct, aligned and non-NULL."""
     a = py()
@@ -90,7 +100,7 @@ def test_cache_append_refusals(L):
         (dict(D=96), EUNSUPPORTED), (dict(D=512), EUNSUPPORTED), (dict(dtype=2), EUNSUPPORTED),
         (dict(page_size=8), EUNSUPPORTED), (dict(k=0x100008), EALIGN), (dict(cache=0x100008), EALIGN),
         (dict(k_row_stride=132), EALIGN), (dict(v_head_stride=68), EALIGN), (dict(v_stored=0x100008), EALIGN),
-        (dict(dtype=0, k_row_stride=130), EALIGN)])
+        (dict(dtype=0, k_row_stride=130), EALIGN), (dict(T=(1 << 24) - 1, Hkv=256, D=256), EINVAL)])
 
 
 def test_cache_attention_refusals(L):
