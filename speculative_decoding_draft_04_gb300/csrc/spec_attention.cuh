@@ -233,48 +233,170 @@ __device__ __forceinline__ void store4(float* p, const float* x) {
   *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
 }
 
+// First head element of lane part t in inner step s of the first product.
+template <int D>
+__device__ __forceinline__ int k_order(int t, int s) {
+  return D == 256 ? (s >> 3) * 128 + 32 * t + 4 * (s & 7) : (D / 4) * t + 4 * s;
+}
+
+// The queries of a row tile in the order of the first product's operand, in
+// NT 16-bit terms; rows are scaled by powers of two so that their largest
+// element is in [2^14, 2^15), which makes bf16 queries exact (elements 2^38
+// below their row's largest aside).  c: what scores are multiplied by, a row.
+template <class C, class DT>
+__device__ __forceinline__ void load_queries(const AttnParams& p, const AttnSeg& sg, uint4* s_q, int lane,
+                                             float (&c)[2 * C::M]) {
+  const int g = lane >> 2, t = lane & 3;
+  const int rows = sg.n * p.G;
+#pragma unroll
+  for (int m = 0; m < C::M; ++m) {
+    float f[2];
+    const DT* src[2];
+    bool live[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = sg.tile * C::ROWS + 16 * m + 8 * e + g;
+      live[e] = r < rows;
+      const int i = live[e] ? r / p.G : 0, hq = sg.h * p.G + (live[e] ? r - i * p.G : 0);
+      src[e] = static_cast<const DT*>(p.q) + (long long)(sg.r0 + i) * p.q_row + hq * p.q_head;
+      float mx = 0.f;
+#pragma unroll
+      for (int s = 0; s < C::KSTEPS; ++s) {
+        float x[4];
+        load4(src[e] + k_order<C::D>(t, s), x);
+        mx = fmaxf(fmaxf(mx, fmaxf(fabsf(x[0]), fabsf(x[1]))), fmaxf(fabsf(x[2]), fabsf(x[3])));
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      int ex = 0;                                        // mx in [2^(ex-1), 2^ex)
+      if (mx > 0.f && mx <= 3.402823466e38f) frexpf(mx, &ex);
+      ex = 15 - ex;
+      ex = ex > 120 ? 120 : ex;
+      const float up = ldexpf(1.f, ex);
+      float cc = fabsf(p.scale) * ldexpf(1.f, -ex);
+      f[e] = p.scale < 0.f ? -up : up;
+      if (!(cc > 0.f)) {                                 // scores of 0
+        f[e] = 0.f;
+        cc = 1.f;
+      }
+      if (!live[e]) f[e] = 0.f;
+      c[2 * m + e] = cc;
+    }
+#pragma unroll
+    for (int s = 0; s < C::KSTEPS; ++s) {
+      float x[2][4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        load4(src[e] + k_order<C::D>(t, s), x[e]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[e][k] = live[e] ? x[e][k] * f[e] : 0.f;
+      }
+#pragma unroll
+      for (int term = 0; term < C::NT; ++term) {
+        uint4 a;
+        a.x = pack_h2(x[0][0], x[0][1]);
+        a.y = pack_h2(x[1][0], x[1][1]);
+        a.z = pack_h2(x[0][2], x[0][3]);
+        a.w = pack_h2(x[1][2], x[1][3]);
+        s_q[((term * C::M + m) * C::KSTEPS + s) * 32 + lane] = a;
+        if (term + 1 < C::NT) {
+          const uint32_t h[2][2] = {{a.x, a.z}, {a.y, a.w}};
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float2 v = half2_floats(h[e][k]);
+              x[e][2 * k] -= v.x;
+              x[e][2 * k + 1] -= v.y;
+            }
+        }
+      }
+    }
+  }
+  __syncwarp();
+}
+
 // Adds the parts of the split segments: CTA (x, y) takes the segments that
-// begin at workers x, x + gridDim.x, .. and eight rows of each.  A part is
+// begin at workers x, x + gridDim.x, .. and JOIN_ROWS rows of each.  A part is
 // [ROWS][D] unnormalised outputs and (m, sum) a row; worker w has slot 0 for a
 // segment that began before its share and slot 1 for one that begins in it.
-constexpr int JOIN_THREADS = 256;
+// Threads that the rows leave over share the parts; the order of every sum
+// depends on the numbers of rows and parts alone.
+constexpr int JOIN_THREADS = 256, JOIN_BATCH = 4;
 template <int D, int ROWS, class DT>
 __global__ void __launch_bounds__(JOIN_THREADS) cache_attention_join_kernel(const __grid_constant__ AttnParams p, int workers) {
+  __shared__ float4 s_acc[JOIN_THREADS];
+  __shared__ float2 s_ml[JOIN_THREADS];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  constexpr int PART = ROWS * D + 2 * ROWS;
+  constexpr int PART = ROWS * D + 2 * ROWS, RQ = D / 4;      // float4 a row
+  constexpr int JOIN_ROWS = JOIN_THREADS / RQ;
   const float* parts = attn_parts(p);
   const AttnSplit* splits = static_cast<const AttnSplit*>(p.ws);
   for (int w = blockIdx.x; w < workers; w += gridDim.x) {
     const AttnSplit s = splits[w];
     if (s.last < s.first) continue;
     const int rows = s.n * p.G;
-    for (int it = threadIdx.x; it < 2 * D; it += JOIN_THREADS) {   // float4 of eight rows
-      const int rl = 8 * blockIdx.y + it / (D / 4), d = 4 * (it % (D / 4));
-      const int r = s.tile * ROWS + rl;
-      if (r >= rows) continue;
-      float m = -INFINITY, sum = 0.f;
+    const int live = min(JOIN_ROWS, rows - s.tile * ROWS - JOIN_ROWS * (int)blockIdx.y);
+    if (live <= 0) continue;                               // uniform over the CTA
+    const int items = live * RQ;
+    // `shares` threads an item: each adds the parts first + own, + shares, ..
+    int shares = JOIN_THREADS / items;
+    if (shares > s.last - s.first + 1) shares = s.last - s.first + 1;
+    if (shares < 1) shares = 1;
+    auto add = [](float2& ml, float4& acc, const float2& v, const float4& o) {
+      const float mn = fmaxf(ml.x, v.x);
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      const float fa = exp2f(ml.x - ref), fb = exp2f(v.x - ref);
+      ml.x = mn;
+      ml.y = ml.y * fa + v.y * fb;
+      acc.x = acc.x * fa + o.x * fb;
+      acc.y = acc.y * fa + o.y * fb;
+      acc.z = acc.z * fa + o.z * fb;
+      acc.w = acc.w * fa + o.w * fb;
+    };
+    {
+      const int own = threadIdx.x / items, it = threadIdx.x - own * items;
+      const bool mine = own < shares;
+      const int rl = JOIN_ROWS * blockIdx.y + it / RQ, d = 4 * (it % RQ);
+      float2 ml = make_float2(-INFINITY, 0.f);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int x = s.first; x <= s.last; ++x) {
-        const float* part = parts + (size_t)(2 * x + (x == s.first ? 1 : 0)) * PART;
-        const float2 v = __ldg(reinterpret_cast<const float2*>(part + ROWS * D + 2 * rl));
-        const float4 o = __ldg(reinterpret_cast<const float4*>(part + rl * D + d));
-        const float mn = fmaxf(m, v.x);
-        const float ref = mn == -INFINITY ? 0.f : mn;
-        const float fa = exp2f(m - ref), fb = exp2f(v.x - ref);
-        m = mn;
-        sum = sum * fa + v.y * fb;
-        acc.x = acc.x * fa + o.x * fb;
-        acc.y = acc.y * fa + o.y * fb;
-        acc.z = acc.z * fa + o.z * fb;
-        acc.w = acc.w * fa + o.w * fb;
+      if (mine) {
+        // JOIN_BATCH parts requested before the first is added
+        for (int x0 = s.first + own; x0 <= s.last; x0 += JOIN_BATCH * shares) {
+          float2 v[JOIN_BATCH];
+          float4 o[JOIN_BATCH];
+#pragma unroll
+          for (int k = 0; k < JOIN_BATCH; ++k) {
+            const int x = x0 + k * shares;
+            v[k] = make_float2(-INFINITY, 0.f);
+            o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (x <= s.last) {
+              const float* part = parts + (size_t)(2 * x + (x == s.first ? 1 : 0)) * PART;
+              v[k] = __ldg(reinterpret_cast<const float2*>(part + ROWS * D + 2 * rl));
+              o[k] = __ldg(reinterpret_cast<const float4*>(part + rl * D + d));
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < JOIN_BATCH; ++k)
+            if (x0 + k * shares <= s.last) add(ml, acc, v[k], o[k]);
+        }
       }
+      if (shares > 1) {
+        __syncthreads();
+        s_acc[threadIdx.x] = acc;
+        s_ml[threadIdx.x] = ml;
+        __syncthreads();
+        if (own == 0)
+          for (int k = 1; k < shares; ++k) add(ml, acc, s_ml[k * items + it], s_acc[k * items + it]);
+      }
+      if (own > 0) continue;
+      const int r = s.tile * ROWS + rl;
       const int tok = r / p.G, hq = s.h * p.G + r - tok * p.G;
       const size_t at = (size_t)(s.r0 + tok) * p.Hq + hq;
-      const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
+      const float inv = ml.y == 0.f ? 0.f : p.v_scale / ml.y;
       const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
       store4(static_cast<DT*>(p.out) + at * D + d, x);
-      if (d == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : 0.69314718056f * (m + log2f(sum));
+      if (d == 0 && p.lse) p.lse[at] = ml.y == 0.f ? -INFINITY : 0.69314718056f * (ml.x + log2f(ml.y));
     }
   }
 }
@@ -284,7 +406,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_attention_join_kernel(cons
 template <int D, int ROWS, class DT>
 cudaError_t launch_attention_join(const AttnParams& p, int workers, int sms, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(workers < 2 * sms ? workers : 2 * sms, ROWS / 8);
+  cfg.gridDim = dim3(workers < 4 * sms ? workers : 4 * sms, (ROWS * D / 4 + JOIN_THREADS - 1) / JOIN_THREADS);
   cfg.blockDim = dim3(JOIN_THREADS);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
