@@ -5,12 +5,12 @@
 //   logprob = (x_token - m) / T - ln Z,     H = ln 2 (log2 Z - sum 2^d d / Z)
 //
 // One read of each row.  logprobs_kernel: a CTA takes one segment of one row,
-// 256 threads x 8 vectors of 16 bytes, all requested at once and kept in
+// 256 threads x 16 vectors of 16 bytes, all requested at once and kept in
 // registers, so that maximum, sums and candidates come from one load.
 //
 // The K largest: a thread's maximum is at hand, so the K-th largest of 64
 // group maxima (4 threads each) is a bound that at least K entries reach and,
-// for values in no particular order, some 10 to 50 of 16384 do.  Those are
+// for values in no particular order, some 10 to 50 of 32768 do.  Those are
 // collected and ranked by counting.  Equal values beyond the list's size (a
 // row of few different values) are found one by one instead.
 //
@@ -37,13 +37,13 @@ struct LogprobParams {
   unsigned long long* keys;               // [rows][segments][K], descending
 };
 
-constexpr int LP_THREADS = 256, LP_WARPS = LP_THREADS / 32, LP_VECS = 8, LP_GROUPS = 64, LP_LIST = 256;
+constexpr int LP_THREADS = 256, LP_WARPS = LP_THREADS / 32, LP_VECS = 16, LP_GROUPS = 64, LP_LIST = 256;
 constexpr float LP_LN2 = 0.69314718056f;
 
 template <class DT>
 struct LpVec {
   static constexpr int E = 16 / sizeof(DT);                  // elements a vector
-  static constexpr int SEG = LP_THREADS * LP_VECS * E;       // elements a segment: 16384 bf16, 8192 fp32
+  static constexpr int SEG = LP_THREADS * LP_VECS * E;       // elements a segment: 32768 bf16, 16384 fp32
 };
 
 // Whole numbers in the order of the floats (-0 counts as 0).
@@ -165,7 +165,7 @@ __device__ __forceinline__ const DT* row_at(const LogprobParams& p, int row) {
 }
 
 template <class DT>
-__global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const __grid_constant__ LogprobParams p) {
+__global__ void __launch_bounds__(LP_THREADS, 2) logprobs_kernel(const __grid_constant__ LogprobParams p) {
   constexpr int E = LpVec<DT>::E, SEG = LpVec<DT>::SEG;
   const DT* const tag = nullptr;
   __shared__ __align__(16) float s_group[LP_GROUPS];
@@ -189,32 +189,42 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const __grid_co
   const int i0 = seg * (SEG / E) + tid;
   uint4 v[LP_VECS];
   float vm[LP_VECS], tm;
-  int edge = -1;                                             // this thread's vector that the row fills in part
+  if (seg * SEG >= lead && (seg + 1) * SEG - lead <= p.V) {  // uniform: a segment that the row fills
+    const uint4* at = reinterpret_cast<const uint4*>(x + (i0 * E - lead));
 #pragma unroll
-  for (int j = 0; j < LP_VECS; ++j) {
-    const int at = (i0 + j * LP_THREADS) * E - lead;
-    const uint32_t w = low_word(tag);
-    v[j] = make_uint4(w, w, w, w);
-    if (at >= 0 && at + E <= p.V) v[j] = __ldcs(reinterpret_cast<const uint4*>(x + at));
-    else if (at + E > 0 && at < p.V) edge = j;
-  }
-  if (edge >= 0) {
-    const uint4 q = edge_vector(x, (i0 + edge * LP_THREADS) * E - lead, p.V);
+    for (int j = 0; j < LP_VECS; ++j) v[j] = __ldcs(at + j * LP_THREADS);
 #pragma unroll
-    for (int j = 0; j < LP_VECS; ++j)
-      if (j == edge) v[j] = q;
+    for (int j = 0; j < LP_VECS; ++j) vm[j] = vec_max(v[j], tag);
+  } else {
+    int edge = -1;                                           // this thread's vector that the row fills in part
+#pragma unroll
+    for (int j = 0; j < LP_VECS; ++j) {
+      const int at = (i0 + j * LP_THREADS) * E - lead;
+      const uint32_t w = low_word(tag);
+      v[j] = make_uint4(w, w, w, w);
+      if (at >= 0 && at + E <= p.V) v[j] = __ldcs(reinterpret_cast<const uint4*>(x + at));
+      else if (at + E > 0 && at < p.V) edge = j;
+    }
+    if (edge >= 0) {
+      const uint4 q = edge_vector(x, (i0 + edge * LP_THREADS) * E - lead, p.V);
+#pragma unroll
+      for (int j = 0; j < LP_VECS; ++j)
+        if (j == edge) v[j] = q;
+    }
+#pragma unroll
+    for (int j = 0; j < LP_VECS; ++j) {
+      const int at = (i0 + j * LP_THREADS) * E - lead;
+      vm[j] = at + E > 0 && at < p.V ? vec_max(v[j], tag) : -INFINITY;
+    }
   }
   if (tid == 0) {
     s_count = 0;
     s_bound = 0;
   }
-  // ---- maxima: vector, thread, group of 8 threads, warp
+  // ---- maxima: thread, group of 4 threads, warp
+  tm = vm[0];
 #pragma unroll
-  for (int j = 0; j < LP_VECS; ++j) {
-    const int at = (i0 + j * LP_THREADS) * E - lead;
-    vm[j] = at + E > 0 && at < p.V ? vec_max(v[j], tag) : -INFINITY;
-  }
-  tm = max_nan(max_nan(max_nan(vm[0], vm[1]), max_nan(vm[2], vm[3])), max_nan(max_nan(vm[4], vm[5]), max_nan(vm[6], vm[7])));
+  for (int j = 1; j < LP_VECS; ++j) tm = max_nan(tm, vm[j]);
   float gm = tm;
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) gm = max_nan(gm, __shfl_xor_sync(0xffffffffu, gm, o));
@@ -429,9 +439,36 @@ __global__ void __launch_bounds__(32 * LPJ_WARPS) logprobs_join_kernel(const __g
     if (p.K == 0) return;
     const unsigned long long* keys = p.keys + (size_t)row * p.segments * p.K;
     unsigned long long mine = 0;                             // lane k keeps the k-th
+    unsigned long long* s_keys = s_lists + warp * (33 * p.K);
+    if (p.segments <= 4) {
+      // few lists: every entry's rank is its place in its own list and, by
+      // bisection, in the others
+      const int total = p.segments * p.K;
+      for (int i = lane; i < total; i += 32) s_keys[i] = keys[i];
+      __syncwarp();
+      for (int i = lane; i < total; i += 32) {
+        const unsigned long long key = s_keys[i];
+        if (key == 0) continue;                              // no entry
+        const int own = i / p.K;
+        int rank = i - own * p.K;
+        for (int s = 0; s < p.segments; ++s)
+          if (s != own) {
+            int lo = 0, hi = p.K;                            // entries of list s above key
+            while (lo < hi) {
+              const int mid = (lo + hi) >> 1;
+              if (s_keys[s * p.K + mid] > key) lo = mid + 1; else hi = mid;
+            }
+            rank += lo;
+          }
+        if (rank < p.K) {
+          p.top_ids[(size_t)row * p.K + rank] = (int)~(uint32_t)key;
+          p.top_lp[(size_t)row * p.K + rank] = (from_ordered((uint32_t)(key >> 32)) - m) / T - lz;
+        }
+      }
+      return;
+    }
     // 32 segments at a time: their sorted lists and the best so far in shared
     // memory, and K times the largest of the lists' heads
-    unsigned long long* s_keys = s_lists + warp * (33 * p.K);
     for (int s0 = 0; s0 < p.segments; s0 += 32) {
       const int lists = min(32, p.segments - s0);
       __syncwarp();
