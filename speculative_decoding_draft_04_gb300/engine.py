@@ -2,7 +2,9 @@
 (torch allocations), owns the output buffers and the workspace, and
 enqueues one speculative cycle (spec_markov_draft then spec_verify) on a
 stream, or the confidence-scheduled cycle (draft, spec_confidence,
-spec_prefix_schedule, then spec_verify with the scheduled lengths).
+spec_prefix_schedule, then spec_verify with the scheduled lengths), or the
+served cycle (draft, room in the paged cache, the target's pass, verify, log
+probabilities of what was emitted).
 Nothing here computes any part of the method."""
 from __future__ import annotations
 
@@ -315,6 +317,135 @@ def tree_cycle(d: DeviceWorkload, t: DeviceTree, stream=None) -> None:
     _lib.spec_tree_verify(t.target, d.U, d.W1, d.W2, d.anchor, d.temperature, t.parent, t.mask,
                           t.tokens, t.u_accept, t.u_final, t.accept_len, t.out_tokens, t.path,
                           t.status, t.workspace, stream)
+
+
+@dataclasses.dataclass
+class DeviceCache:
+    """The paged 4-bit cache of a target model's layers and the requests in it.
+
+    Lengths, page counts and ring positions are kept twice: every step reads
+    one set and writes the other.  ``row_ptr``, ``slots`` and ``positions``
+    describe the packed rows of the newest step."""
+    page_size: int
+    layers: list            # uint8 [num_pages][Hkv][page_size / 16][18 D] each
+    k_scale: list
+    v_scale: list
+    softmax_scale: float
+    seq_len: list           # two sets
+    num_blocks: list
+    ring_pos: list
+    newest: int
+    free_ring: object
+    block_table: object
+    kv_len: object
+    row_ptr: object
+    slots: object
+    positions: object
+    status: object
+    workspace: object
+
+    @classmethod
+    def allocate(cls, B, layers, Hq, Hkv, D, page_size, num_pages, max_tokens, max_rows, k_scale,
+                 v_scale, softmax_scale=None, device="cuda") -> "DeviceCache":
+        """Empty requests of up to max_tokens tokens, every page free; k_scale
+        and v_scale: one number per layer."""
+        import torch
+        if len(k_scale) != layers or len(v_scale) != layers:
+            raise _lib.SpecError("k_scale and v_scale need one number per layer")
+        if _lib.spec_cache_bytes(num_pages, Hkv, page_size, D) == 0:
+            raise _lib.SpecError("unsupported cache shape for libspec")
+        nbytes = _lib.spec_cache_attention_workspace_bytes(Hq, Hkv, D)
+        if nbytes == 0:
+            raise _lib.SpecError("unsupported heads for libspec")
+        o = dict(device=device)
+
+        def i32(*shape):
+            return torch.zeros(shape, dtype=torch.int32, **o)
+
+        ring = torch.zeros((2, 2), dtype=torch.int64)
+        ring[0, 1] = num_pages
+        ring = ring.to(device)
+        return cls(page_size=page_size,
+                   layers=[torch.zeros((num_pages, Hkv, page_size // 16, 18 * D), dtype=torch.uint8, **o)
+                           for _ in range(layers)],
+                   k_scale=list(k_scale), v_scale=list(v_scale),
+                   softmax_scale=D ** -0.5 if softmax_scale is None else softmax_scale,
+                   seq_len=[i32(B), i32(B)], num_blocks=[i32(B), i32(B)], ring_pos=[ring[0], ring[1]],
+                   newest=0, free_ring=torch.arange(num_pages, dtype=torch.int32, **o),
+                   block_table=torch.full((B, -(-max_tokens // page_size)), -1, dtype=torch.int32, **o),
+                   kv_len=i32(B), row_ptr=i32(B + 1), slots=i32(max_rows), positions=i32(max_rows),
+                   status=i32(4), workspace=torch.empty(nbytes, dtype=torch.uint8, **o))
+
+
+def make_room(c: DeviceCache, new_len, accept_len=None, stream=None) -> None:
+    """Keep what the last block's verification accepted and make room for each
+    request's new_len next tokens.  accept_len counts the kept tokens of the
+    last block beyond its first (prompt length - 1 after a prompt); None keeps
+    nothing of it, as before the first block."""
+    old, new = c.newest, 1 - c.newest
+    _lib.spec_block_tables(c.seq_len[old], accept_len, new_len, c.num_blocks[old], c.ring_pos[old],
+                           c.free_ring, c.block_table, c.seq_len[new], c.kv_len, c.num_blocks[new],
+                           c.ring_pos[new], c.row_ptr, c.slots, c.positions, c.status, c.page_size,
+                           stream=stream)
+    c.newest = new
+
+
+def attend(c: DeviceCache, layer: int, q, k, v, out, tree_mask=None, lse=None, stream=None) -> None:
+    """One layer's attention of the newest step's packed rows: their keys and
+    values go into the cache, their queries over it.  q, k, v: [T][heads][D]
+    with T at most the rows that the step was made for."""
+    _lib.spec_cache_append(k, v, c.slots[:k.shape[0]], c.layers[layer], c.status, c.k_scale[layer],
+                           c.v_scale[layer], stream=stream)
+    _lib.spec_cache_attention(q, c.layers[layer], c.block_table, c.kv_len, c.row_ptr, out, c.status,
+                              c.workspace, c.softmax_scale, c.k_scale[layer], c.v_scale[layer],
+                              tree_mask=tree_mask, lse=lse, stream=stream)
+
+
+@dataclasses.dataclass
+class DeviceLogprobs:
+    """What is reported about the emitted tokens."""
+    logprob: object
+    entropy: object
+    top_ids: object
+    top_logprobs: object
+    status: object
+    workspace: object
+
+    @classmethod
+    def allocate(cls, B, n, V, K=0, device="cuda") -> "DeviceLogprobs":
+        import torch
+        o = dict(device=device)
+        nbytes = _lib.spec_logprobs_workspace_bytes(B * n, V, K)
+        if nbytes == 0:
+            raise _lib.SpecError("unsupported shape for libspec")
+        return cls(logprob=torch.empty((B, n), dtype=torch.float32, **o),
+                   entropy=torch.empty((B, n), dtype=torch.float32, **o),
+                   top_ids=torch.empty((B, n, K), dtype=torch.int32, **o) if K else None,
+                   top_logprobs=torch.empty((B, n, K), dtype=torch.float32, **o) if K else None,
+                   status=torch.zeros(4, dtype=torch.int32, **o),
+                   workspace=torch.empty(nbytes, dtype=torch.uint8, **o))
+
+
+def logprobs(logits, tokens, temperature, l: DeviceLogprobs, stream=None) -> None:
+    _lib.spec_logprobs(logits, tokens, l.logprob, l.entropy, l.status, l.workspace,
+                       temperature=temperature, top_ids=l.top_ids, top_logprobs=l.top_logprobs,
+                       stream=stream)
+
+
+def served_cycle(d: DeviceWorkload, b: Buffers, c: DeviceCache, l: DeviceLogprobs, target_pass,
+                 new_len, accept_len=None, stream=None) -> None:
+    """One cycle of a server: draft, keep what the last cycle accepted and make
+    room for the block, the target's pass over it, verify, and the log
+    probabilities of the emitted tokens.  target_pass(d, b, c, stream) enqueues
+    the model's layers, each with ``attend``, and leaves its logits in
+    d.target; new_len is gamma + 1 per request (the anchor and the block), 1 +
+    verify_len where lengths are scheduled.  b.accept_len of this cycle is
+    accept_len of the next."""
+    draft(d, b, stream)
+    make_room(c, new_len, accept_len, stream)
+    target_pass(d, b, c, stream)
+    verify(d, b, stream)
+    logprobs(d.target, b.out_tokens, d.temperature, l, stream)
 
 
 def status_words(t) -> list[int]:
