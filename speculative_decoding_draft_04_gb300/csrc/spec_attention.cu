@@ -37,42 +37,546 @@
 
 namespace spec {
 
-// Geometry of a kernel: head size, row tiles of 16, terms of a 16-bit split.
+// A query row of this lane: its D / 4 elements of the order above, and what they
+// are multiplied by.  Rows are scaled by powers of two so that their largest
+// element is in [2^14, 2^15), which makes bf16 queries exact in 16-bit floats
+// (elements 2^38 below their row's largest aside); c is what the scores are
+// multiplied by in turn.
+template <int D, class DT>
+struct QueryRow {
+  const DT* src;
+  float f, c;
+  bool live;
+  __device__ __forceinline__ QueryRow(const AttnParams& p, const AttnSeg& sg, int r, int t) {
+    live = r < sg.n * p.G;
+    const int i = live ? r / p.G : 0, hq = sg.h * p.G + (live ? r - i * p.G : 0);
+    src = static_cast<const DT*>(p.q) + (long long)(sg.r0 + i) * p.q_row + hq * p.q_head;
+    float mx = 0.f;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      float x[4];
+      load4(src + k_order<D>(t, s), x);
+      mx = fmaxf(fmaxf(mx, fmaxf(fabsf(x[0]), fabsf(x[1]))), fmaxf(fabsf(x[2]), fabsf(x[3])));
+    }
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    int ex = 0;                                          // mx in [2^(ex-1), 2^ex)
+    if (mx > 0.f && mx <= 3.402823466e38f) frexpf(mx, &ex);
+    ex = 15 - ex;
+    ex = ex > 120 ? 120 : ex;
+    const float up = ldexpf(1.f, ex);
+    f = p.scale < 0.f ? -up : up;
+    c = fabsf(p.scale) * ldexpf(1.f, -ex);
+    if (!(c > 0.f)) {                                    // scores of 0
+      f = 0.f;
+      c = 1.f;
+    }
+  }
+  // Four elements of inner step s in NT 16-bit terms.
+  template <int NT>
+  __device__ __forceinline__ void terms(int t, int s, uint2 (&a)[NT]) const {
+    float x[4];
+    load4(src + k_order<D>(t, s), x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = live ? x[k] * f : 0.f;
+#pragma unroll
+    for (int term = 0; term < NT; ++term) {
+      a[term] = make_uint2(pack_h2(x[0], x[1]), pack_h2(x[2], x[3]));
+      const float2 lo = half2_floats(a[term].x), hi = half2_floats(a[term].y);
+      x[0] -= lo.x; x[1] -= lo.y; x[2] -= hi.x; x[3] -= hi.y;
+    }
+  }
+};
+
+// Codes and scales of a unit's K, four tokens a lane: tokens (g / 2) + 4 (g % 2)
+// + 8 j of the two blocks, the D / 4 elements of part t.
+template <class C>
+__device__ __forceinline__ void load_k(const uint8_t* unit, int g, int t, uint32_t (&kc)[4][C::KW], uint32_t (&ks)[4][C::KG]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int tok = (g >> 1) + 4 * (g & 1) + 8 * (j & 1);
+    const uint8_t* blk = unit + (j >> 1) * (18 * C::D);
+    const uint8_t* row = blk + tok * (C::D / 2);
+    if (C::D == 64) {
+      const uint2 v = *reinterpret_cast<const uint2*>(row + 8 * t);
+      kc[j][0] = v.x; kc[j][1] = v.y;
+    } else {
+#pragma unroll
+      for (int h = 0; h < C::D / 128; ++h) {
+        const uint4 v = *reinterpret_cast<const uint4*>(row + 64 * h + 16 * t);
+        kc[j][4 * h] = v.x; kc[j][4 * h + 1] = v.y; kc[j][4 * h + 2] = v.z; kc[j][4 * h + 3] = v.w;
+      }
+    }
+    const uint8_t* sc = blk + cache_k_scales(C::D) + tok * (C::D / 16);
+    if (C::D == 64) {
+      const uint32_t two = decode_scales(sc[t]);
+      ks[j][0] = __byte_perm(two, two, 0x1010);
+    } else {
+#pragma unroll
+      for (int h = 0; h < C::D / 128; ++h) {
+        const uint32_t two = decode_scales(*reinterpret_cast<const uint16_t*>(sc + 8 * h + 2 * t));
+        ks[j][2 * h] = __byte_perm(two, two, 0x1010);
+        ks[j][2 * h + 1] = __byte_perm(two, two, 0x3232);
+      }
+    }
+  }
+}
+// Codes and scales of a block's V, D / 8 elements (from D / 8 g on) of four tokens
+// a lane.  tokens t and t + 4 in one word, t + 8 and t + 12 in the other: the
+// even elements' codes side by side in `even`, the odd ones' in `odd`
+template <class C>
+__device__ __forceinline__ void load_v(const uint8_t* blk, int g, int t, uint32_t (&even)[2][C::VW], uint32_t (&odd)[2][C::VW],
+                                       uint32_t (&vs)[2][2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t a[C::VW], b[C::VW], sa, sb;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int tok = t + 8 * i + 4 * e;
+      const uint8_t* row = blk + cache_v_codes(C::D) + tok * (C::D / 2) + g * (C::D / 16);
+      uint32_t* w = e ? b : a;
+      if (C::D == 64) {
+        w[0] = *reinterpret_cast<const uint32_t*>(row);
+      } else if (C::D == 128) {
+        const uint2 v = *reinterpret_cast<const uint2*>(row);
+        w[0] = v.x; w[C::VW - 1] = v.y;
+      } else {
+        const uint4 v = *reinterpret_cast<const uint4*>(row);
+        w[0] = v.x; w[1 % C::VW] = v.y; w[2 % C::VW] = v.z; w[3 % C::VW] = v.w;
+      }
+      const uint8_t* sc = blk + cache_v_scales(C::D) + tok * (C::D / 16);
+      uint32_t two = C::D == 256 ? *reinterpret_cast<const uint16_t*>(sc + 2 * g)
+                                 : (uint32_t)sc[C::D == 128 ? g : g >> 1];
+      if (e) sb = two; else sa = two;
+    }
+    vs[i][0] = decode_scales(__byte_perm(sa, sb, 0x0040));
+    vs[i][1] = C::D == 256 ? decode_scales(__byte_perm(sa, sb, 0x0051)) : vs[i][0];
+#pragma unroll
+    for (int w = 0; w < C::VW; ++w) {
+      even[i][w] = (a[w] & 0x0f0f0f0fu) | ((b[w] << 4) & 0xf0f0f0f0u);
+      odd[i][w] = ((a[w] >> 4) & 0x0f0f0f0fu) | (b[w] & 0xf0f0f0f0u);
+    }
+  }
+}
+// Bytes of tokens that nobody wrote: V scales of 0 (after the last read of K's).
+template <class C>
+__device__ __forceinline__ void clear_unwritten(const uint8_t* unit, int tok0, int L, int lane) {
+  if (tok0 + lane >= L) {
+    uint8_t* sc = const_cast<uint8_t*>(unit) + (lane >> 4) * (18 * C::D) + cache_v_scales(C::D) + (lane & 15) * (C::D / 16);
+#pragma unroll
+    for (int i = 0; i < C::D / 64; ++i) reinterpret_cast<uint32_t*>(sc)[i] = 0;
+  }
+  fence_async_shared();                                  // before the stage's next copy
+  __syncwarp();
+}
+// Whether a row sees token tok (>= ctx: a new one).  lim: tokens that it sees
+// (causal) or its packed row (tree mask); -1 where there is no row.
+__device__ __forceinline__ bool sees(const AttnParams& p, int tok, int lim, int ctx, int L) {
+  if (!p.mask) return tok < lim;
+  const int d = tok - ctx;
+  if (lim < 0 || tok >= L) return false;
+  return d < 0 || ((d >> 5) < p.mask_words && ((__ldg(p.mask + (size_t)lim * p.mask_words + (d >> 5)) >> (d & 31)) & 1u));
+}
+
+// Products with query rows along the operands' 16 rows: M tiles of 16.
 template <int D_, int M_, int NT_>
-struct AttnCfg {
-  static constexpr int D = D_, M = M_, NT = NT_;
-  static constexpr int ROWS = 16 * M;
-  static constexpr int KSTEPS = D / 16;
-  static constexpr int KW = D / 32;                     // K code words a lane and token
-  static constexpr int KG = D / 64;                     // K scales a lane and token
-  static constexpr int NV = D / 8;                      // V columns a lane and token = output tiles
-  static constexpr int VW = D >= 128 ? D / 64 : 1;      // V code words a lane and token (D = 64: 4 bytes)
-  static constexpr int UNIT_BYTES = 2 * 18 * D;
-  static constexpr int Q_BYTES = NT * M * KSTEPS * 512;
+struct RowTiles {
+  using C = RowTiles;
+  static constexpr int D = D_, M = M_, NT = NT_, ROWS = 16 * M;
+  static constexpr int KSTEPS = D / 16, KW = D / 32, KG = D / 64, NV = D / 8, VW = D >= 128 ? D / 64 : 1;
+  static constexpr int Q_BYTES = NT * ROWS * KSTEPS * 32;
   // 12 warps of 168 registers where 8 of 255 are not needed; two CTAs of 8 for small heads
   static constexpr int MIN_CTAS = M == 1 && NT == 1 && D == 64 ? 2 : 1;
   static constexpr int WARPS = D == 256 && NT == 2 ? 4 : D == 128 && M == 1 && NT == 1 ? 12 : 8;
-  static constexpr int WARP_BUDGET = (MIN_CTAS == 2 ? 110 : 220) * 1024 / WARPS;
-  static constexpr int FIT = (WARP_BUDGET - Q_BYTES) / UNIT_BYTES;
+  float c[2 * M], mref[2 * M], O[M][NV][4], l[2 * M];    // l: this lane's tokens
+  int lim[2 * M];
+  bool upper;                                            // rows 8 .. of the tile exist
+
+  template <class DT>
+  __device__ __forceinline__ void begin(const AttnParams& p, const AttnSeg& sg, uint4* s_q, int lane) {
+    const int g = lane >> 2, t = lane & 3, rows = sg.n * p.G;
+    upper = M > 1 || rows - sg.tile * ROWS > 8;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const QueryRow<D, DT> lo(p, sg, sg.tile * ROWS + 16 * m + g, t), hi(p, sg, sg.tile * ROWS + 16 * m + 8 + g, t);
+      c[2 * m] = lo.c;
+      c[2 * m + 1] = hi.c;
+#pragma unroll
+      for (int s = 0; s < KSTEPS; ++s) {
+        uint2 a[NT], b[NT];
+        lo.terms(t, s, a);
+        hi.terms(t, s, b);
+#pragma unroll
+        for (int term = 0; term < NT; ++term)
+          s_q[((term * M + m) * KSTEPS + s) * 32 + lane] = make_uint4(a[term].x, b[term].x, a[term].y, b[term].y);
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2 * M; ++i) {
+      mref[i] = -INFINITY;
+      l[i] = 0.f;
+      const int r = sg.tile * ROWS + 16 * (i >> 1) + 8 * (i & 1) + g;
+      lim[i] = r < rows ? (p.mask ? sg.r0 + r / p.G : sg.L - sg.n + r / p.G + 1) : -1;
+    }
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) O[m][j][k] = 0.f;
+  }
+
+  __device__ __forceinline__ void pass(const AttnParams& p, const AttnSeg& sg, const uint4* s_q, const uint8_t* unit, int u,
+                                       int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    // ---- first product: scores of 4 x 8 tokens
+    float S[M][4][4];
+    uint32_t kc[4][KW], ks[4][KG];
+    load_k<C>(unit, g, t, kc, ks);
+#pragma unroll
+    for (int s = 0; s < KSTEPS; ++s) {
+      uint4 a[NT][M];
+#pragma unroll
+      for (int term = 0; term < NT; ++term)
+#pragma unroll
+        for (int m = 0; m < M; ++m) a[term][m] = s_q[((term * M + m) * KSTEPS + s) * 32 + lane];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t b0 = mul_h2(decode_byte(kc[j], 2 * s), ks[j][s >> 2]);
+        const uint32_t b1 = mul_h2(decode_byte(kc[j], 2 * s + 1), ks[j][s >> 2]);
+#pragma unroll
+        for (int term = 0; term < NT; ++term)
+#pragma unroll
+          for (int m = 0; m < M; ++m) {
+            if (s == 0 && term == 0) mma_f16_first(S[m][j], a[term][m], b0, b1);
+            else mma_f16(S[m][j], a[term][m], b0, b1);
+          }
+      }
+    }
+    // ---- masks, where the unit reaches the new tokens
+    const int tok0 = u * AT_UNIT, ctx = sg.L - sg.n;
+    if (tok0 + AT_UNIT > ctx) {
+      clear_unwritten<C>(unit, tok0, sg.L, lane);
+#pragma unroll
+      for (int i = 0; i < 2 * M; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (!sees(p, tok0 + 16 * (j >> 1) + 8 * (j & 1) + t + 4 * e, lim[i], ctx, sg.L))
+              S[i >> 1][j][2 * (i & 1) + e] = -INFINITY;
+    }
+    // ---- probabilities
+    float top[2 * M];
+    bool far = false;
+#pragma unroll
+    for (int i = 0; i < 2 * M; ++i) {
+      const int m = i >> 1, e = 2 * (i & 1);
+      float x = fmaxf(S[m][0][e], S[m][0][e + 1]);
+#pragma unroll
+      for (int j = 1; j < 4; ++j) x = max3(x, S[m][j][e], S[m][j][e + 1]);
+      top[i] = x;
+      far |= c[i] * (x - mref[i]) > AT_SLACK;
+    }
+    if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+      for (int i = 0; i < 2 * M; ++i) {
+        float x = top[i];
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+        x = fmaxf(x, mref[i]);
+        const float f = x == mref[i] ? 1.f : exp2_approx(c[i] * (mref[i] - x));
+        mref[i] = x;
+        const int m = i >> 1, e = 2 * (i & 1);
+        l[i] *= f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          O[m][j][e] *= f;
+          O[m][j][e + 1] *= f;
+        }
+      }
+    }
+    uint4 pa[NT][M][2];
+#pragma unroll
+    for (int i = 0; i < 2 * M; ++i) {
+      const int m = i >> 1, e = 2 * (i & 1);
+      if (i == 1 && !upper) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) S[m][j][e] = S[m][j][e + 1] = 0.f;
+        continue;
+      }
+      const float base = mref[i] == -INFINITY ? 0.f : AT_SHIFT - c[i] * mref[i];
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          S[m][j][e + k] = exp2_approx(fmaf(S[m][j][e + k], c[i], base));
+          sum += S[m][j][e + k];
+        }
+      l[i] += sum;
+    }
+#pragma unroll
+    for (int term = 0; term < NT; ++term)
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint4 a;
+          a.x = pack_h2(S[m][2 * k][0], S[m][2 * k][1]);
+          a.y = pack_h2(S[m][2 * k][2], S[m][2 * k][3]);
+          a.z = pack_h2(S[m][2 * k + 1][0], S[m][2 * k + 1][1]);
+          a.w = pack_h2(S[m][2 * k + 1][2], S[m][2 * k + 1][3]);
+          pa[term][m][k] = a;
+          if (term + 1 < NT) {
+            const uint32_t h[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float2 v = half2_floats(h[q]);
+              S[m][2 * k + (q >> 1)][2 * (q & 1)] -= v.x;
+              S[m][2 * k + (q >> 1)][2 * (q & 1) + 1] -= v.y;
+            }
+          }
+        }
+    // ---- second product, 16 tokens a step
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint32_t even[2][VW], odd[2][VW], vs[2][2];
+      load_v<C>(unit + k * (18 * D), g, t, even, odd, vs);
+#pragma unroll
+      for (int jj = 0; jj < NV / 2; ++jj) {
+        const int sg2 = C::D == 256 ? jj >> 3 : 0;
+        const uint32_t b0 = mul_h2(decode_byte(even[0], jj), vs[0][sg2]), b1 = mul_h2(decode_byte(even[1], jj), vs[1][sg2]);
+        const uint32_t d0 = mul_h2(decode_byte(odd[0], jj), vs[0][sg2]), d1 = mul_h2(decode_byte(odd[1], jj), vs[1][sg2]);
+#pragma unroll
+        for (int term = 0; term < NT; ++term)
+#pragma unroll
+          for (int m = 0; m < M; ++m) {
+            mma_f16(O[m][2 * jj], pa[term][m][k], b0, b1);
+            mma_f16(O[m][2 * jj + 1], pa[term][m][k], d0, d1);
+          }
+      }
+    }
+  }
+
+  // The lanes' sums added up.
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int i = 0; i < 2 * M; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    }
+  }
+  // Sums i, 0 .. 2 M - 1: their row in the tile; four elements at a time of the
+  // lane's part of it; and whether the lane writes (m, sum).
+  static constexpr int SUMS = 2 * M, QUADS = NV / 2;
+  __device__ __forceinline__ static int row(int i, int lane) { return 16 * (i >> 1) + 8 * (i & 1) + (lane >> 2); }
+  __device__ __forceinline__ static int column(int q, int lane) {
+    return (2 * (lane & 3) + q / (NV / 4)) * NV + 4 * (q % (NV / 4));
+  }
+  __device__ __forceinline__ void quad(int i, int q, float (&x)[4]) const {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) x[v] = O[i >> 1][4 * (q % (NV / 4)) + v][2 * (i & 1) + q / (NV / 4)];
+  }
+  __device__ __forceinline__ static bool first(int lane) { return (lane & 3) == 0; }
+};
+
+// Products with tokens (first) and head elements (second) along the operands' 16
+// rows and 8 query rows along their columns, for tiles of no more rows: half the
+// products and half the softmax of a 16-row tile.  The first product's result
+// becomes the second's operand by transposing 8x8 tiles of it.
+template <int D_, int NT_>
+struct ColumnTile {
+  using C = ColumnTile;
+  static constexpr int D = D_, NT = NT_, ROWS = 8;
+  static constexpr int KSTEPS = D / 16, KW = D / 32, KG = D / 64, NV = D / 8, VW = D >= 128 ? D / 64 : 1;
+  static constexpr int Q_BYTES = NT * ROWS * KSTEPS * 32;
+  static constexpr int MIN_CTAS = NT == 1 && D == 64 ? 2 : 1;
+  static constexpr int WARPS = D == 128 && NT == 1 ? 12 : 8;
+  float c[2], mref[2], O[NV / 2][4], l[2];               // rows 2 t and 2 t + 1; l: this lane's tokens
+  int lim[2];
+
+  template <class DT>
+  __device__ __forceinline__ void begin(const AttnParams& p, const AttnSeg& sg, uint4* s_q, int lane) {
+    const int g = lane >> 2, t = lane & 3, rows = sg.n * p.G;
+    const QueryRow<D, DT> q(p, sg, sg.tile * ROWS + g, t);
+#pragma unroll
+    for (int s = 0; s < KSTEPS; s += 2) {
+      uint2 a[NT], b[NT];
+      q.terms(t, s, a);
+      q.terms(t, s + 1, b);
+#pragma unroll
+      for (int term = 0; term < NT; ++term)
+        s_q[(term * (KSTEPS / 2) + s / 2) * 32 + lane] = make_uint4(a[term].x, a[term].y, b[term].x, b[term].y);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      c[i] = __shfl_sync(0xffffffffu, q.c, 8 * t + 4 * i);
+      mref[i] = -INFINITY;
+      l[i] = 0.f;
+      const int r = sg.tile * ROWS + 2 * t + i;
+      lim[i] = r < rows ? (p.mask ? sg.r0 + r / p.G : sg.L - sg.n + r / p.G + 1) : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < NV / 2; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) O[j][k] = 0.f;
+  }
+
+  __device__ __forceinline__ void pass(const AttnParams& p, const AttnSeg& sg, const uint4* s_q, const uint8_t* unit, int u,
+                                       int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    // ---- first product: scores of 2 x 16 tokens
+    float S[2][4];
+    uint32_t kc[4][KW], ks[4][KG];
+    load_k<C>(unit, g, t, kc, ks);
+#pragma unroll
+    for (int s = 0; s < KSTEPS; ++s) {
+      uint4 a[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        a[i].x = mul_h2(decode_byte(kc[2 * i], 2 * s), ks[2 * i][s >> 2]);
+        a[i].y = mul_h2(decode_byte(kc[2 * i + 1], 2 * s), ks[2 * i + 1][s >> 2]);
+        a[i].z = mul_h2(decode_byte(kc[2 * i], 2 * s + 1), ks[2 * i][s >> 2]);
+        a[i].w = mul_h2(decode_byte(kc[2 * i + 1], 2 * s + 1), ks[2 * i + 1][s >> 2]);
+      }
+#pragma unroll
+      for (int term = 0; term < NT; ++term) {
+        const uint2 b = reinterpret_cast<const uint2*>(s_q)[((term * (KSTEPS / 2) + s / 2) * 32 + lane) * 2 + (s & 1)];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (s == 0 && term == 0) mma_f16_first(S[i], a[i], b.x, b.y);
+          else mma_f16(S[i], a[i], b.x, b.y);
+        }
+      }
+    }
+    // ---- masks, where the unit reaches the new tokens
+    const int tok0 = u * AT_UNIT, ctx = sg.L - sg.n;
+    if (tok0 + AT_UNIT > ctx) {
+      clear_unwritten<C>(unit, tok0, sg.L, lane);
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (!sees(p, tok0 + 16 * i + 8 * e + (g >> 1) + 4 * (g & 1), lim[r], ctx, sg.L)) S[i][2 * e + r] = -INFINITY;
+    }
+    // ---- probabilities
+    float top[2];
+    bool far = false;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      top[r] = max3(fmaxf(S[0][r], S[0][r + 2]), S[1][r], S[1][r + 2]);
+      far |= c[r] * (top[r] - mref[r]) > AT_SLACK;
+    }
+    if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float x = top[r];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+        x = fmaxf(x, mref[r]);
+        const float f = x == mref[r] ? 1.f : exp2_approx(c[r] * (mref[r] - x));
+        mref[r] = x;
+        l[r] *= f;
+#pragma unroll
+        for (int j = 0; j < NV / 2; ++j) {
+          O[j][r] *= f;
+          O[j][r + 2] *= f;
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float base = mref[r] == -INFINITY ? 0.f : AT_SHIFT - c[r] * mref[r];
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          S[i][r + 2 * k] = exp2_approx(fmaf(S[i][r + 2 * k], c[r], base));
+          sum += S[i][r + 2 * k];
+        }
+      l[r] += sum;
+    }
+    uint32_t pb[NT][2][2];
+#pragma unroll
+    for (int term = 0; term < NT; ++term)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t h = pack_h2(S[i][2 * k], S[i][2 * k + 1]);
+          pb[term][i][k] = transpose8(h);
+          if (term + 1 < NT) {
+            const float2 v = half2_floats(h);
+            S[i][2 * k] -= v.x;
+            S[i][2 * k + 1] -= v.y;
+          }
+        }
+    // ---- second product, 16 tokens a step
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint32_t even[2][VW], odd[2][VW], vs[2][2];
+      load_v<C>(unit + k * (18 * D), g, t, even, odd, vs);
+#pragma unroll
+      for (int jj = 0; jj < NV / 2; ++jj) {
+        const int sg2 = D == 256 ? jj >> 3 : 0;
+        uint4 a;
+        a.x = mul_h2(decode_byte(even[0], jj), vs[0][sg2]);
+        a.y = mul_h2(decode_byte(odd[0], jj), vs[0][sg2]);
+        a.z = mul_h2(decode_byte(even[1], jj), vs[1][sg2]);
+        a.w = mul_h2(decode_byte(odd[1], jj), vs[1][sg2]);
+#pragma unroll
+        for (int term = 0; term < NT; ++term) mma_f16(O[jj], a, pb[term][k][0], pb[term][k][1]);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+  }
+  static constexpr int SUMS = 2, QUADS = NV / 4;
+  __device__ __forceinline__ static int row(int i, int lane) { return 2 * (lane & 3) + i; }
+  __device__ __forceinline__ static int column(int q, int lane) { return (lane >> 2) * NV + 4 * q; }
+  __device__ __forceinline__ void quad(int i, int q, float (&x)[4]) const {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) x[v] = O[2 * q + (v >> 1)][i + 2 * (v & 1)];
+  }
+  __device__ __forceinline__ static bool first(int lane) { return lane < 4; }
+};
+
+// Shared memory of a kernel, and the floats of a part: [ROWS][D] outputs, then
+// (m, sum) a row.
+template <class C>
+struct AttnCfg {
+  static constexpr int UNIT_BYTES = 2 * 18 * C::D;
+  static constexpr int WARP_BUDGET = (C::MIN_CTAS == 2 ? 110 : 220) * 1024 / C::WARPS;
+  static constexpr int FIT = (WARP_BUDGET - C::Q_BYTES) / UNIT_BYTES;
   static constexpr int DEPTH = FIT > 6 ? 6 : FIT;
-  static constexpr int WARP_BYTES = Q_BYTES + DEPTH * UNIT_BYTES;
-  static constexpr int SMEM = WARPS * WARP_BYTES;
-  // floats of a part: [ROWS][D] outputs, then (m, sum) a row
-  static constexpr int PART = ROWS * D + 2 * ROWS;
+  static constexpr int WARP_BYTES = C::Q_BYTES + DEPTH * UNIT_BYTES;
+  static constexpr int SMEM = C::WARPS * WARP_BYTES;
+  static constexpr int PART = C::ROWS * C::D + 2 * C::ROWS;
   static_assert(DEPTH >= 2, "ring");
 };
 
 template <class C, class DT>
 __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_kernel(const __grid_constant__ AttnParams p) {
+  using F = AttnCfg<C>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t s_bar[C::WARPS][C::DEPTH];
+  __shared__ __align__(8) uint64_t s_bar[C::WARPS][F::DEPTH];
   __shared__ long long s_pre[32 * C::WARPS + 1];         // units before each group of requests
   __shared__ long long s_scan[C::WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, t = lane & 3;
   uint64_t* bar = s_bar[warp];
 
-  if (lane < C::DEPTH) mbar_init(bar + lane, 1);
+  if (lane < F::DEPTH) mbar_init(bar + lane, 1);
   const long long total = attn_prefix<C::ROWS, AT_UNIT, 32 * C::WARPS>(p, s_pre, s_scan, [] { __syncthreads(); });
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -84,8 +588,8 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
   float* parts = attn_parts(p);
   AttnSplit* splits = static_cast<AttnSplit*>(p.ws);
   AttnSplit split{0, -1, 0, 0, 0, 0, 0};
-  uint8_t* ring = smem + warp * C::WARP_BYTES;
-  uint4* s_q = reinterpret_cast<uint4*>(ring + C::DEPTH * C::UNIT_BYTES);
+  uint8_t* ring = smem + warp * F::WARP_BYTES;
+  uint4* s_q = reinterpret_cast<uint4*>(ring + F::DEPTH * F::UNIT_BYTES);
 
   if (begin < end) {
     auto locate = [&](long long at) { return attn_locate<C::ROWS, AT_UNIT, 32 * C::WARPS>(p, s_pre, at); };
@@ -115,7 +619,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
       src = p.cache + ((size_t)page * p.Hkv + ps.h) * head_bytes;
       if (big) {
         const int in_page = (tok & (p.P - 1)) / AT_UNIT, left = p.P / AT_UNIT - in_page;
-        src += (size_t)in_page * C::UNIT_BYTES;
+        src += (size_t)in_page * F::UNIT_BYTES;
         run = min(min(left, ps.nu - ps.u), end - ppos < left ? (int)(end - ppos) : left);
         next = page_id(tok + left * AT_UNIT);
       } else {
@@ -127,25 +631,25 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
     auto issue = [&]() {
       if (run == 0) refill();
       uint64_t* ibar = bar + istage;
-      uint8_t* dst = ring + istage * C::UNIT_BYTES;
+      uint8_t* dst = ring + istage * F::UNIT_BYTES;
       if (big) {
         if (lane == 0) {
-          expect_bytes(ibar, C::UNIT_BYTES);
-          bulk_load(dst, src, C::UNIT_BYTES, ibar);
+          expect_bytes(ibar, F::UNIT_BYTES);
+          bulk_load(dst, src, F::UNIT_BYTES, ibar);
         }
-        src += C::UNIT_BYTES;
+        src += F::UNIT_BYTES;
       } else {
-        if (lane == 0) expect_bytes(ibar, second ? C::UNIT_BYTES : C::UNIT_BYTES / 2);
+        if (lane == 0) expect_bytes(ibar, second ? F::UNIT_BYTES : F::UNIT_BYTES / 2);
         __syncwarp();
         if (lane == 0 || (lane == 1 && second))
-          bulk_load(dst + lane * (C::UNIT_BYTES / 2), src, C::UNIT_BYTES / 2, ibar);
+          bulk_load(dst + lane * (F::UNIT_BYTES / 2), src, F::UNIT_BYTES / 2, ibar);
       }
-      if (++istage == C::DEPTH) istage = 0;
+      if (++istage == F::DEPTH) istage = 0;
       --run;
       ++ps.u;
       ++ppos;
     };
-    for (int i = 0; i < C::DEPTH && ppos < end; ++i) issue();
+    for (int i = 0; i < F::DEPTH && ppos < end; ++i) issue();
     int cstage = 0;
     uint32_t cphase = 0;
     bool timed_out = false;
@@ -155,23 +659,9 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
       const AttnSeg sg = locate(pos);
       const int u_first = sg.u;
       const int u_end = sg.nu - sg.u < end - pos ? sg.nu : sg.u + (int)(end - pos);
-      const int rows = sg.n * p.G, ctx = sg.L - sg.n;
-      float c[2 * C::M], mref[2 * C::M], O[C::M][C::NV][4], l[2 * C::M];   // l: this lane's columns
-      load_queries<C, DT>(p, sg, s_q, lane, c);
-      int lim[2 * C::M];                                 // tokens a row sees (causal), its packed row
-#pragma unroll
-      for (int i = 0; i < 2 * C::M; ++i) {
-        mref[i] = -INFINITY;
-        l[i] = 0.f;
-        const int r = sg.tile * C::ROWS + 16 * (i >> 1) + 8 * (i & 1) + g;
-        lim[i] = r < rows ? (p.mask ? sg.r0 + r / p.G : ctx + r / p.G + 1) : -1;
-      }
-#pragma unroll
-      for (int m = 0; m < C::M; ++m)
-#pragma unroll
-        for (int j = 0; j < C::NV; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) O[m][j][k] = 0.f;
+      const int rows = sg.n * p.G;
+      C tile;
+      tile.template begin<DT>(p, sg, s_q, lane);
       bool poison = sg.bad;                              // a page outside the cache in this part
       if (!sg.bad) {
         const int tok_end = min(sg.L, u_end * AT_UNIT);
@@ -183,7 +673,6 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
         poison = __any_sync(0xffffffffu, bad);
         if (poison && lane == 0) set_status(p.status, SPEC_DEV_BAD_SLOT);
       }
-      const bool upper = C::M > 1 || rows - sg.tile * C::ROWS > 8;   // rows 8.. of the tile exist
 
       for (int u = u_first; u < u_end; ++u) {
         if (!bar_wait(bar + cstage, cphase)) timed_out = true;
@@ -193,215 +682,8 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
           poison = true;
           break;
         }
-        {
-          const uint8_t* unit = ring + cstage * C::UNIT_BYTES;
-          // ---- first product: scores of 4 x 8 tokens
-          float S[C::M][4][4];
-          uint32_t kc[4][C::KW], ks[4][C::KG];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int tok = (g >> 1) + 4 * (g & 1) + 8 * (j & 1);
-            const uint8_t* blk = unit + (j >> 1) * (18 * C::D);
-            const uint8_t* row = blk + tok * (C::D / 2);
-            if (C::D == 64) {
-              const uint2 v = *reinterpret_cast<const uint2*>(row + 8 * t);
-              kc[j][0] = v.x; kc[j][1] = v.y;
-            } else {
-#pragma unroll
-              for (int h = 0; h < C::D / 128; ++h) {
-                const uint4 v = *reinterpret_cast<const uint4*>(row + 64 * h + 16 * t);
-                kc[j][4 * h] = v.x; kc[j][4 * h + 1] = v.y; kc[j][4 * h + 2] = v.z; kc[j][4 * h + 3] = v.w;
-              }
-            }
-            const uint8_t* sc = blk + cache_k_scales(C::D) + tok * (C::D / 16);
-            if (C::D == 64) {
-              const uint32_t two = decode_scales(sc[t]);
-              ks[j][0] = __byte_perm(two, two, 0x1010);
-            } else {
-#pragma unroll
-              for (int h = 0; h < C::D / 128; ++h) {
-                const uint32_t two = decode_scales(*reinterpret_cast<const uint16_t*>(sc + 8 * h + 2 * t));
-                ks[j][2 * h] = __byte_perm(two, two, 0x1010);
-                ks[j][2 * h + 1] = __byte_perm(two, two, 0x3232);
-              }
-            }
-          }
-#pragma unroll
-          for (int s = 0; s < C::KSTEPS; ++s) {
-            uint4 a[C::NT][C::M];
-#pragma unroll
-            for (int term = 0; term < C::NT; ++term)
-#pragma unroll
-              for (int m = 0; m < C::M; ++m) a[term][m] = s_q[((term * C::M + m) * C::KSTEPS + s) * 32 + lane];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t b0 = mul_h2(decode_byte(kc[j], 2 * s), ks[j][s >> 2]);
-              const uint32_t b1 = mul_h2(decode_byte(kc[j], 2 * s + 1), ks[j][s >> 2]);
-#pragma unroll
-              for (int term = 0; term < C::NT; ++term)
-#pragma unroll
-                for (int m = 0; m < C::M; ++m) {
-                  if (s == 0 && term == 0) mma_f16_first(S[m][j], a[term][m], b0, b1);
-                  else mma_f16(S[m][j], a[term][m], b0, b1);
-                }
-            }
-          }
-          // ---- masks, where the unit reaches the new tokens
-          const int tok0 = u * AT_UNIT;
-          const bool edge = tok0 + AT_UNIT > ctx;
-          if (edge) {
-            // bytes that nobody wrote: V scales of 0 (the last read of K's is above)
-            const int t0 = tok0 + lane;
-            if (t0 >= sg.L) {
-              uint8_t* sc = const_cast<uint8_t*>(unit) + (lane >> 4) * (18 * C::D) + cache_v_scales(C::D) + (lane & 15) * (C::D / 16);
-#pragma unroll
-              for (int i = 0; i < C::D / 64; ++i) reinterpret_cast<uint32_t*>(sc)[i] = 0;
-            }
-            fence_async_shared();                        // before the stage's next copy
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 2 * C::M; ++i)
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int tok = tok0 + 16 * (j >> 1) + 8 * (j & 1) + t + 4 * e;
-                  bool seen = tok < lim[i];
-                  if (p.mask) {
-                    const int d = tok - ctx;
-                    seen = lim[i] >= 0 && tok < sg.L;
-                    if (seen && d >= 0)
-                      seen = (d >> 5) < p.mask_words &&
-                             ((__ldg(p.mask + (size_t)lim[i] * p.mask_words + (d >> 5)) >> (d & 31)) & 1u);
-                  }
-                  if (!seen) S[i >> 1][j][2 * (i & 1) + e] = -INFINITY;
-                }
-          }
-          // ---- probabilities
-          float top[2 * C::M];
-          bool far = false;
-#pragma unroll
-          for (int i = 0; i < 2 * C::M; ++i) {
-            const int m = i >> 1, e = 2 * (i & 1);
-            float x = fmaxf(S[m][0][e], S[m][0][e + 1]);
-#pragma unroll
-            for (int j = 1; j < 4; ++j) x = max3(x, S[m][j][e], S[m][j][e + 1]);
-            top[i] = x;
-            far |= c[i] * (x - mref[i]) > AT_SLACK;
-          }
-          if (__any_sync(0xffffffffu, far)) {
-#pragma unroll
-            for (int i = 0; i < 2 * C::M; ++i) {
-              float x = top[i];
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-              x = fmaxf(x, mref[i]);
-              const float f = x == mref[i] ? 1.f : exp2_approx(c[i] * (mref[i] - x));
-              mref[i] = x;
-              const int m = i >> 1, e = 2 * (i & 1);
-              l[i] *= f;
-#pragma unroll
-              for (int j = 0; j < C::NV; ++j) {
-                O[m][j][e] *= f;
-                O[m][j][e + 1] *= f;
-              }
-            }
-          }
-          uint4 pa[C::NT][C::M][2];
-#pragma unroll
-          for (int i = 0; i < 2 * C::M; ++i) {
-            const int m = i >> 1, e = 2 * (i & 1);
-            if (i == 1 && !upper) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) S[m][j][e] = S[m][j][e + 1] = 0.f;
-              continue;
-            }
-            const float base = mref[i] == -INFINITY ? 0.f : AT_SHIFT - c[i] * mref[i];
-            float sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                S[m][j][e + k] = exp2_approx(fmaf(S[m][j][e + k], c[i], base));
-                sum += S[m][j][e + k];
-              }
-            l[i] += sum;
-          }
-#pragma unroll
-          for (int term = 0; term < C::NT; ++term)
-#pragma unroll
-            for (int m = 0; m < C::M; ++m)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                uint4 a;
-                a.x = pack_h2(S[m][2 * k][0], S[m][2 * k][1]);
-                a.y = pack_h2(S[m][2 * k][2], S[m][2 * k][3]);
-                a.z = pack_h2(S[m][2 * k + 1][0], S[m][2 * k + 1][1]);
-                a.w = pack_h2(S[m][2 * k + 1][2], S[m][2 * k + 1][3]);
-                pa[term][m][k] = a;
-                if (term + 1 < C::NT) {
-                  const uint32_t h[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                  for (int q = 0; q < 4; ++q) {
-                    const float2 v = half2_floats(h[q]);
-                    S[m][2 * k + (q >> 1)][2 * (q & 1)] -= v.x;
-                    S[m][2 * k + (q >> 1)][2 * (q & 1) + 1] -= v.y;
-                  }
-                }
-              }
-          // ---- second product, 16 tokens a step
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint8_t* blk = unit + k * (18 * C::D);
-            // tokens t and t + 4 in one word, t + 8 and t + 12 in the other: the
-            // even elements' codes side by side in `even`, the odd ones' in `odd`
-            uint32_t even[2][C::VW], odd[2][C::VW], vs[2][2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              uint32_t a[C::VW], b[C::VW], sa, sb;
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int tok = t + 8 * i + 4 * e;
-                const uint8_t* row = blk + cache_v_codes(C::D) + tok * (C::D / 2) + g * (C::D / 16);
-                uint32_t* w = e ? b : a;
-                if (C::D == 64) {
-                  w[0] = *reinterpret_cast<const uint32_t*>(row);
-                } else if (C::D == 128) {
-                  const uint2 v = *reinterpret_cast<const uint2*>(row);
-                  w[0] = v.x; w[C::VW - 1] = v.y;
-                } else {
-                  const uint4 v = *reinterpret_cast<const uint4*>(row);
-                  w[0] = v.x; w[1 % C::VW] = v.y; w[2 % C::VW] = v.z; w[3 % C::VW] = v.w;
-                }
-                const uint8_t* sc = blk + cache_v_scales(C::D) + tok * (C::D / 16);
-                uint32_t two = C::D == 256 ? *reinterpret_cast<const uint16_t*>(sc + 2 * g)
-                                           : (uint32_t)sc[C::D == 128 ? g : g >> 1];
-                if (e) sb = two; else sa = two;
-              }
-              vs[i][0] = decode_scales(__byte_perm(sa, sb, 0x0040));
-              vs[i][1] = C::D == 256 ? decode_scales(__byte_perm(sa, sb, 0x0051)) : vs[i][0];
-#pragma unroll
-              for (int w = 0; w < C::VW; ++w) {
-                even[i][w] = (a[w] & 0x0f0f0f0fu) | ((b[w] << 4) & 0xf0f0f0f0u);
-                odd[i][w] = ((a[w] >> 4) & 0x0f0f0f0fu) | (b[w] & 0xf0f0f0f0u);
-              }
-            }
-#pragma unroll
-            for (int jj = 0; jj < C::NV / 2; ++jj) {
-              const int sg2 = C::D == 256 ? jj >> 3 : 0;
-              const uint32_t b0 = mul_h2(decode_byte(even[0], jj), vs[0][sg2]), b1 = mul_h2(decode_byte(even[1], jj), vs[1][sg2]);
-              const uint32_t d0 = mul_h2(decode_byte(odd[0], jj), vs[0][sg2]), d1 = mul_h2(decode_byte(odd[1], jj), vs[1][sg2]);
-#pragma unroll
-              for (int term = 0; term < C::NT; ++term)
-#pragma unroll
-                for (int m = 0; m < C::M; ++m) {
-                  mma_f16(O[m][2 * jj], pa[term][m][k], b0, b1);
-                  mma_f16(O[m][2 * jj + 1], pa[term][m][k], d0, d1);
-                }
-            }
-          }
-        }
-        if (++cstage == C::DEPTH) {
+        tile.pass(p, sg, s_q, ring + cstage * F::UNIT_BYTES, u, lane);
+        if (++cstage == F::DEPTH) {
           cstage = 0;
           cphase ^= 1u;
         }
@@ -411,53 +693,39 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
 
       // ---- the segment's end in this share
       const bool whole = u_first == 0 && u_end == sg.nu;
+      tile.finish();
+      const int slot = u_first == 0 ? 1 : 0;             // 0: the segment began before this share
+      float* part = parts + (size_t)(2 * me + slot) * F::PART;
 #pragma unroll
-      for (int i = 0; i < 2 * C::M; ++i) {
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        if (poison) l[i] = quiet_nan();
-      }
-      if (whole) {
-#pragma unroll
-        for (int i = 0; i < 2 * C::M; ++i) {
-          const int m = i >> 1, e = 2 * (i & 1);
-          const int r = sg.tile * C::ROWS + 16 * m + 8 * (i & 1) + g;
-          if (r >= rows) continue;
+      for (int i = 0; i < C::SUMS; ++i) {
+        const int rl = C::row(i, lane), r = sg.tile * C::ROWS + rl;
+        if (r >= rows) continue;
+        const float sum = poison ? quiet_nan() : tile.l[i];
+        const float m = tile.mref[i] == -INFINITY ? -INFINITY : tile.c[i] * tile.mref[i] - AT_SHIFT;
+        if (whole) {
           const int tok = r / p.G, hq = sg.h * p.G + r - tok * p.G;
-          const float sum = l[i];
           const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
           const size_t at = (size_t)(sg.r0 + tok) * p.Hq + hq;
-          DT* o = static_cast<DT*>(p.out) + at * C::D;
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+          for (int q = 0; q < C::QUADS; ++q) {
+            float x[4];
+            tile.quad(i, q, x);
 #pragma unroll
-            for (int j = 0; j < C::NV; j += 4) {
-              const float x[4] = {O[m][j][e + k] * inv, O[m][j + 1][e + k] * inv, O[m][j + 2][e + k] * inv,
-                                  O[m][j + 3][e + k] * inv};
-              store4(o + (2 * t + k) * C::NV + j, x);
-            }
-          if (t == 0 && p.lse)
-            p.lse[at] = sum == 0.f ? -INFINITY : 0.69314718056f * (c[i] * mref[i] - AT_SHIFT + log2f(sum));
+            for (int v = 0; v < 4; ++v) x[v] *= inv;
+            store4(static_cast<DT*>(p.out) + at * C::D + C::column(q, lane), x);
+          }
+          if (C::first(lane) && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : 0.69314718056f * (m + log2f(sum));
+        } else {
+#pragma unroll
+          for (int q = 0; q < C::QUADS; ++q) {
+            float x[4];
+            tile.quad(i, q, x);
+            store4(part + rl * C::D + C::column(q, lane), x);
+          }
+          if (C::first(lane)) *reinterpret_cast<float2*>(part + C::ROWS * C::D + 2 * rl) = make_float2(m, sum);
         }
-      } else {
-        // slot 0: the segment began before this share; slot 1: it begins here
-        const int slot = u_first == 0 ? 1 : 0;
-        float* part = parts + (size_t)(2 * me + slot) * C::PART;
-#pragma unroll
-        for (int i = 0; i < 2 * C::M; ++i) {
-          const int m = i >> 1, e = 2 * (i & 1);
-          const int rl = 16 * m + 8 * (i & 1) + g;
-          if (sg.tile * C::ROWS + rl >= rows) continue;
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int j = 0; j < C::NV; j += 4)
-              *reinterpret_cast<float4*>(part + rl * C::D + (2 * t + k) * C::NV + j) =
-                  make_float4(O[m][j][e + k], O[m][j + 1][e + k], O[m][j + 2][e + k], O[m][j + 3][e + k]);
-          if (t == 0)
-            *reinterpret_cast<float2*>(part + C::ROWS * C::D + 2 * rl) =
-                make_float2(mref[i] == -INFINITY ? -INFINITY : c[i] * mref[i] - AT_SHIFT, l[i]);
-        }
+      }
+      if (!whole) {
         if (slot == 1) {
           const long long seg_last = pos + (sg.nu - 1);  // the segment's last unit
           split = AttnSplit{me, (int)(seg_last / share), sg.b, sg.h, sg.tile, sg.n, sg.r0};
@@ -466,9 +734,9 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
       pos += u_end - u_first;
     }
     if (timed_out)                                       // leave no copy in flight
-      for (int i = 0; i < C::DEPTH; ++i) {
+      for (int i = 0; i < F::DEPTH; ++i) {
         bar_wait(bar + cstage, cphase);
-        if (++cstage == C::DEPTH) {
+        if (++cstage == F::DEPTH) {
           cstage = 0;
           cphase ^= 1u;
         }
@@ -480,14 +748,15 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
 namespace {
 template <class C, class DT>
 cudaError_t launch_cfg(const AttnParams& p, int sms, cudaStream_t st) {
-  static_assert(C::SMEM <= 227 * 1024 - 4096, "shared memory");
+  using F = AttnCfg<C>;
+  static_assert(F::SMEM <= 227 * 1024 - 4096, "shared memory");
   // once a device: the attribute stays with the function
   static std::atomic<uint64_t> sized{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !((sized.load(std::memory_order_relaxed) >> dev) & 1)) {
-    e = cudaFuncSetAttribute(cache_attention_kernel<C, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    e = cudaFuncSetAttribute(cache_attention_kernel<C, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
     if (e != cudaSuccess) return e;
     if (dev < 64) sized.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
@@ -497,7 +766,7 @@ cudaError_t launch_cfg(const AttnParams& p, int sms, cudaStream_t st) {
   const long long tiles = (long long)p.T * p.G / C::ROWS + (p.T < p.B ? p.T : p.B);
   const long long units = tiles * p.Hkv * (((long long)p.stride * p.P + AT_UNIT - 1) / AT_UNIT);
   if (ctas > units) ctas = units;
-  cache_attention_kernel<C, DT><<<(int)ctas, 32 * C::WARPS, C::SMEM, st>>>(p);
+  cache_attention_kernel<C, DT><<<(int)ctas, 32 * C::WARPS, F::SMEM, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_attention_join<C::D, C::ROWS, DT>(p, (int)ctas * C::WARPS, sms, st);
 }
@@ -516,20 +785,30 @@ cudaError_t launch_cache_attention(const spec_cache_attention_args& a, int sms, 
   AttnParams p{a.B, a.T, a.Hq, a.Hkv, G, a.page_size, a.num_pages, a.table_stride, a.mask_words, a.q, a.q_row_stride,
                a.q_head_stride, a.cache, a.block_table, a.kv_len, a.row_ptr, a.tree_mask,
                a.softmax_scale * a.k_scale * 1.4426950408889634f, a.v_scale, a.out, a.lse, a.dev_status, a.workspace};
-  if (a.dtype == SPEC_F32) {
-    if (a.D == 64) return launch_cfg<AttnCfg<64, 1, 2>, float>(p, sms, st);
-    if (a.D == 128) return launch_cfg<AttnCfg<128, 1, 2>, float>(p, sms, st);
-    return launch_cfg<AttnCfg<256, 1, 2>, float>(p, sms, st);
-  }
-  // 16-row tiles (12 warps of 168 registers), but 32-row tiles (8 warps of 255)
-  // where the mean request nearly fills one: 4 x 90k tokens take 237 us in two
-  // 16-row tiles and 199 us in one of 32; with 8 to 32 rows a request (mean 20)
-  // 128 x 4k tokens take 290 and 305 us, with 100 rows 32 x 2k 267 and 290 us.
+  // Tiles of 8 rows where the mean request has no more: one token of 32
+  // requests (4 query heads a key-value head, 265k tokens held) takes 91 us in
+  // them and 107 us in 16-row tiles.  Else 16-row tiles (12 warps of 168 registers), but
+  // 32-row tiles (8 warps of 255) where the mean request nearly fills one: 4 x
+  // 90k tokens take 237 us in two 16-row tiles and 199 us in one of 32; with 8 to
+  // 32 rows a request (mean 20) 128 x 4k tokens take 290 and 305 us, with 100
+  // rows 32 x 2k 267 and 290 us.
   const long long rows = (long long)a.T * G;
-  const bool wide = rows > 24LL * a.B && rows <= 32LL * a.B;
-  if (a.D == 64) return wide ? launch_cfg<AttnCfg<64, 2, 1>, bf16>(p, sms, st) : launch_cfg<AttnCfg<64, 1, 1>, bf16>(p, sms, st);
-  if (a.D == 128) return wide ? launch_cfg<AttnCfg<128, 2, 1>, bf16>(p, sms, st) : launch_cfg<AttnCfg<128, 1, 1>, bf16>(p, sms, st);
-  return launch_cfg<AttnCfg<256, 1, 1>, bf16>(p, sms, st);
+  const bool few = rows <= 8LL * a.B, wide = rows > 24LL * a.B && rows <= 32LL * a.B;
+  if (a.dtype == SPEC_F32) {
+    if (a.D == 64) return few ? launch_cfg<ColumnTile<64, 2>, float>(p, sms, st) : launch_cfg<RowTiles<64, 1, 2>, float>(p, sms, st);
+    if (a.D == 128)
+      return few ? launch_cfg<ColumnTile<128, 2>, float>(p, sms, st) : launch_cfg<RowTiles<128, 1, 2>, float>(p, sms, st);
+    return few ? launch_cfg<ColumnTile<256, 2>, float>(p, sms, st) : launch_cfg<RowTiles<256, 1, 2>, float>(p, sms, st);
+  }
+  if (a.D == 64)
+    return few    ? launch_cfg<ColumnTile<64, 1>, bf16>(p, sms, st)
+           : wide ? launch_cfg<RowTiles<64, 2, 1>, bf16>(p, sms, st)
+                  : launch_cfg<RowTiles<64, 1, 1>, bf16>(p, sms, st);
+  if (a.D == 128)
+    return few    ? launch_cfg<ColumnTile<128, 1>, bf16>(p, sms, st)
+           : wide ? launch_cfg<RowTiles<128, 2, 1>, bf16>(p, sms, st)
+                  : launch_cfg<RowTiles<128, 1, 1>, bf16>(p, sms, st);
+  return few ? launch_cfg<ColumnTile<256, 1>, bf16>(p, sms, st) : launch_cfg<RowTiles<256, 1, 1>, bf16>(p, sms, st);
 }
 
 }  // namespace spec

@@ -184,6 +184,12 @@ __device__ __forceinline__ void mma_f16_first(float* c, const uint4& a, uint32_t
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
 }
+// An 8x8 matrix of 16-bit floats, a row's pair a lane, to its transpose.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
 __device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -239,83 +245,6 @@ __device__ __forceinline__ int k_order(int t, int s) {
   return D == 256 ? (s >> 3) * 128 + 32 * t + 4 * (s & 7) : (D / 4) * t + 4 * s;
 }
 
-// The queries of a row tile in the order of the first product's operand, in
-// NT 16-bit terms; rows are scaled by powers of two so that their largest
-// element is in [2^14, 2^15), which makes bf16 queries exact (elements 2^38
-// below their row's largest aside).  c: what scores are multiplied by, a row.
-template <class C, class DT>
-__device__ __forceinline__ void load_queries(const AttnParams& p, const AttnSeg& sg, uint4* s_q, int lane,
-                                             float (&c)[2 * C::M]) {
-  const int g = lane >> 2, t = lane & 3;
-  const int rows = sg.n * p.G;
-#pragma unroll
-  for (int m = 0; m < C::M; ++m) {
-    float f[2];
-    const DT* src[2];
-    bool live[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = sg.tile * C::ROWS + 16 * m + 8 * e + g;
-      live[e] = r < rows;
-      const int i = live[e] ? r / p.G : 0, hq = sg.h * p.G + (live[e] ? r - i * p.G : 0);
-      src[e] = static_cast<const DT*>(p.q) + (long long)(sg.r0 + i) * p.q_row + hq * p.q_head;
-      float mx = 0.f;
-#pragma unroll
-      for (int s = 0; s < C::KSTEPS; ++s) {
-        float x[4];
-        load4(src[e] + k_order<C::D>(t, s), x);
-        mx = fmaxf(fmaxf(mx, fmaxf(fabsf(x[0]), fabsf(x[1]))), fmaxf(fabsf(x[2]), fabsf(x[3])));
-      }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      int ex = 0;                                        // mx in [2^(ex-1), 2^ex)
-      if (mx > 0.f && mx <= 3.402823466e38f) frexpf(mx, &ex);
-      ex = 15 - ex;
-      ex = ex > 120 ? 120 : ex;
-      const float up = ldexpf(1.f, ex);
-      float cc = fabsf(p.scale) * ldexpf(1.f, -ex);
-      f[e] = p.scale < 0.f ? -up : up;
-      if (!(cc > 0.f)) {                                 // scores of 0
-        f[e] = 0.f;
-        cc = 1.f;
-      }
-      if (!live[e]) f[e] = 0.f;
-      c[2 * m + e] = cc;
-    }
-#pragma unroll
-    for (int s = 0; s < C::KSTEPS; ++s) {
-      float x[2][4];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        load4(src[e] + k_order<C::D>(t, s), x[e]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x[e][k] = live[e] ? x[e][k] * f[e] : 0.f;
-      }
-#pragma unroll
-      for (int term = 0; term < C::NT; ++term) {
-        uint4 a;
-        a.x = pack_h2(x[0][0], x[0][1]);
-        a.y = pack_h2(x[1][0], x[1][1]);
-        a.z = pack_h2(x[0][2], x[0][3]);
-        a.w = pack_h2(x[1][2], x[1][3]);
-        s_q[((term * C::M + m) * C::KSTEPS + s) * 32 + lane] = a;
-        if (term + 1 < C::NT) {
-          const uint32_t h[2][2] = {{a.x, a.z}, {a.y, a.w}};
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float2 v = half2_floats(h[e][k]);
-              x[e][2 * k] -= v.x;
-              x[e][2 * k + 1] -= v.y;
-            }
-        }
-      }
-    }
-  }
-  __syncwarp();
-}
-
 // Adds the parts of the split segments: CTA (x, y) takes the segments that
 // begin at workers x, x + gridDim.x, .. and JOIN_ROWS rows of each.  A part is
 // [ROWS][D] unnormalised outputs and (m, sum) a row; worker w has slot 0 for a
@@ -329,7 +258,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_attention_join_kernel(cons
   __shared__ float2 s_ml[JOIN_THREADS];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   constexpr int PART = ROWS * D + 2 * ROWS, RQ = D / 4;      // float4 a row
-  constexpr int JOIN_ROWS = JOIN_THREADS / RQ;
+  constexpr int JOIN_ROWS = JOIN_THREADS / RQ < ROWS ? JOIN_THREADS / RQ : ROWS;
   const float* parts = attn_parts(p);
   const AttnSplit* splits = static_cast<const AttnSplit*>(p.ws);
   for (int w = blockIdx.x; w < workers; w += gridDim.x) {
