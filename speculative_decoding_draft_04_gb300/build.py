@@ -19,7 +19,7 @@ OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libspec.so")
 SOURCES = ["spec_abi.cu", "spec_draft.cu", "spec_draft_slice.cu", "spec_verify.cu",
            "spec_verify_slice.cu", "spec_verify_redecide.cu", "spec_refine.cu", "spec_report.cu",
-           "spec_sched.cu", "spec_tree.cu", "spec_tables.cu", "spec_cache.cu", "spec_attention.cu",
+           "spec_sched.cu", "spec_tree.cu", "spec_tables.cu", "spec_cache.cu", "spec_attention.cu", "spec_attention_tc.cu",
            "spec_logprobs.cu"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 NVCC_FLAGS = [ARCH, "-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",

@@ -60,13 +60,10 @@ struct QueryRow {
     }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    int ex = 0;                                          // mx in [2^(ex-1), 2^ex)
-    if (mx > 0.f && mx <= 3.402823466e38f) frexpf(mx, &ex);
-    ex = 15 - ex;
-    ex = ex > 120 ? 120 : ex;
-    const float up = ldexpf(1.f, ex);
+    const int ex = query_exponent(mx);
+    const float up = power_of_2(ex);
     f = p.scale < 0.f ? -up : up;
-    c = fabsf(p.scale) * ldexpf(1.f, -ex);
+    c = fabsf(p.scale) * power_of_2(-ex);
     if (!(c > 0.f)) {                                    // scores of 0
       f = 0.f;
       c = 1.f;
@@ -593,6 +590,9 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
 
   if (begin < end) {
     auto locate = [&](long long at) { return attn_locate<C::ROWS, AT_UNIT, 32 * C::WARPS>(p, s_pre, at); };
+    auto following = [&](const AttnSeg& s, long long at) {
+      return attn_next<C::ROWS, AT_UNIT, 32 * C::WARPS>(p, s_pre, s, at);
+    };
     const int bpp = p.P / CACHE_BLOCK, page_bits = 31 - __clz(p.P);
     const size_t head_bytes = (size_t)bpp * cache_block_bytes(C::D);
 
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
     int next = page_id(ps.u * AT_UNIT + (big ? 0 : (lane & 1) * CACHE_BLOCK));
     auto refill = [&]() {
       if (ps.u >= ps.nu) {
-        ps = locate(ppos);
+        ps = following(ps, ppos);
         next = page_id(ps.u * AT_UNIT + (big ? 0 : (lane & 1) * CACHE_BLOCK));
       }
       const int tok = ps.u * AT_UNIT;
@@ -655,8 +655,9 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
     bool timed_out = false;
 
     long long pos = begin;
+    AttnSeg next_sg = locate(begin);
     while (pos < end && !timed_out) {
-      const AttnSeg sg = locate(pos);
+      const AttnSeg sg = next_sg;
       const int u_first = sg.u;
       const int u_end = sg.nu - sg.u < end - pos ? sg.nu : sg.u + (int)(end - pos);
       const int rows = sg.n * p.G;
@@ -732,6 +733,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
         }
       }
       pos += u_end - u_first;
+      if (pos < end) next_sg = following(sg, pos);
     }
     if (timed_out)                                       // leave no copy in flight
       for (int i = 0; i < F::DEPTH; ++i) {
@@ -790,8 +792,7 @@ cudaError_t launch_cache_attention(const spec_cache_attention_args& a, int sms, 
   // them and 107 us in 16-row tiles.  Else 16-row tiles (12 warps of 168 registers), but
   // 32-row tiles (8 warps of 255) where the mean request nearly fills one: 4 x
   // 90k tokens take 237 us in two 16-row tiles and 199 us in one of 32; with 8 to
-  // 32 rows a request (mean 20) 128 x 4k tokens take 290 and 305 us, with 100
-  // rows 32 x 2k 267 and 290 us.
+  // 32 rows a request (mean 20) 128 x 4k tokens take 290 and 305 us.
   const long long rows = (long long)a.T * G;
   const bool few = rows <= 8LL * a.B, wide = rows > 24LL * a.B && rows <= 32LL * a.B;
   if (a.dtype == SPEC_F32) {
@@ -800,6 +801,10 @@ cudaError_t launch_cache_attention(const spec_cache_attention_args& a, int sms, 
       return few ? launch_cfg<ColumnTile<128, 2>, float>(p, sms, st) : launch_cfg<RowTiles<128, 1, 2>, float>(p, sms, st);
     return few ? launch_cfg<ColumnTile<256, 2>, float>(p, sms, st) : launch_cfg<RowTiles<256, 1, 2>, float>(p, sms, st);
   }
+  // above a mean of 32 rows, 128-row tiles: 34 rows of 128 x 4k tokens take 406 us
+  // in them and in 16-row tiles, 50 rows 418 and 570; trees of 100 rows over 32 x
+  // 2k 126 and 265
+  if (a.D <= 128 && rows > 32LL * a.B) return launch_cache_attention_tc(p, a.D, sms, st);
   if (a.D == 64)
     return few    ? launch_cfg<ColumnTile<64, 1>, bf16>(p, sms, st)
            : wide ? launch_cfg<RowTiles<64, 2, 1>, bf16>(p, sms, st)

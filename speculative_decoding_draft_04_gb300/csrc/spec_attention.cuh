@@ -245,6 +245,30 @@ __device__ __forceinline__ int k_order(int t, int s) {
   return D == 256 ? (s >> 3) * 128 + 32 * t + 4 * (s & 7) : (D / 4) * t + 4 * s;
 }
 
+// The segment after one that ended, whose first unit is `pos`: most often the
+// same request's.
+template <int ROWS, int UNIT, int THREADS>
+__device__ __forceinline__ AttnSeg attn_next(const AttnParams& p, const long long* s_pre, const AttnSeg& seg, long long pos) {
+  AttnSeg s = seg;
+  s.u = 0;
+  if (++s.tile * ROWS < s.n * p.G) return s;
+  s.tile = 0;
+  if (++s.h < p.Hkv) return s;
+  return attn_locate<ROWS, UNIT, THREADS>(p, s_pre, pos);
+}
+
+// The power of two that takes mx into [2^14, 2^15) (at most 2^120; 2^15 for 0,
+// infinities and NaN), as its exponent.
+__device__ __forceinline__ int query_exponent(float mx) {
+  const uint32_t u = __float_as_uint(mx);
+  if (!(mx > 0.f && mx <= 3.402823466e38f)) return 15;
+  return min(15 + 126 - (int)(u >> 23), 120);
+}
+__device__ __forceinline__ float power_of_2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126 .. 127
+
+// The kernel of 128-row tiles (bf16, D = 64 or 128).
+cudaError_t launch_cache_attention_tc(const AttnParams& p, int D, int sms, cudaStream_t st);
+
 // Adds the parts of the split segments: CTA (x, y) takes the segments that
 // begin at workers x, x + gridDim.x, .. and JOIN_ROWS rows of each.  A part is
 // [ROWS][D] unnormalised outputs and (m, sum) a row; worker w has slot 0 for a
