@@ -214,53 +214,69 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
     // ------------------------------------------------ softmax
     const uint32_t trow = tmem + ((uint32_t)(32 * warp) << 16);
     uint32_t i = 0;
+    const int rl = 32 * warp + lane;                         // this thread's row
+    uint8_t* const qrow = sm + rl * 128;
     AttnSeg next = locate(begin);
+    int ntok = 0, nhq = 0;                                   // the row's new token and query head; < 0: none
+    // Copies the warp's queries of segment `next` to their place, D / 8 lanes a
+    // row: once the last products of the segment before have read that.
+    auto copy_queries = [&]() {
+      constexpr int LANES = D / 8, PER = 32 / LANES;         // rows an instruction
+      const int r = next.tile * TA_ROWS + rl;
+      const bool there = r < next.n * p.G;
+      ntok = there ? r / p.G : -1;
+      nhq = next.h * p.G + (there ? r - ntok * p.G : 0);
+      const long long off = there ? (long long)(next.r0 + ntok) * p.q_row + nhq * p.q_head : -1;
+      const int ch = lane % LANES;
+#pragma unroll
+      for (int k = 0; k < LANES; ++k) {
+        const int j = k * PER + lane / LANES, rw = 32 * warp + j;
+        const long long from = __shfl_sync(0xffffffffu, off, j);
+        cp_async16(sm + (ch >> 3) * (TA_ROWS * 128) + rw * 128 + (((ch & 7) ^ (rw & 7)) << 4),
+                   static_cast<const bf16*>(p.q) + (from < 0 ? 0 : from) + 8 * ch, from >= 0);
+      }
+      cp_async_commit();
+    };
+    copy_queries();
     for (long long pos = begin; pos < end;) {
       const AttnSeg sg = next;
       const int u_first = sg.u;
       const int u_end = sg.nu - sg.u < end - pos ? sg.nu : sg.u + (int)(end - pos);
-      const int rows = sg.n * p.G, ctx = sg.L - sg.n;
-      const int rl = 32 * warp + lane, r = sg.tile * TA_ROWS + rl;
-      const bool live = r < rows;
-      const int tok = live ? r / p.G : 0, hq = sg.h * p.G + (live ? r - tok * p.G : 0);
-      // ---- this warp's queries, D / 8 lanes a row; scaled by a power of two so
-      // that a row's largest element is in [2^14, 2^15), which makes bf16 exact in
-      // 16-bit floats (elements 2^38 below it aside).  The last segment's products
-      // are done.
-      constexpr int LANES = D / 8, PER = 32 / LANES;         // rows an instruction
-      float c = 1.f;
-#pragma unroll
-      for (int k0 = 0; k0 < 32 / PER; k0 += 8) {
-        uint4 v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int rr = sg.tile * TA_ROWS + 32 * warp + (k0 + k) * PER + lane / LANES;
-          const int ti = rr < rows ? rr / p.G : 0, hi = sg.h * p.G + (rr < rows ? rr - ti * p.G : 0);
-          const bf16* src = static_cast<const bf16*>(p.q) + (long long)(sg.r0 + ti) * p.q_row + hi * p.q_head;
-          v[k] = rr < rows ? __ldg(reinterpret_cast<const uint4*>(src) + lane % LANES) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-          float mx = 0.f;
+      const long long after = pos + (u_end - u_first);
+      const int ctx = sg.L - sg.n;
+      const bool live = ntok >= 0;
+      const int tok = live ? ntok : 0, hq = nhq;
+      // ---- this thread's query as 16-bit floats, scaled by a power of two so that
+      // its largest element is in [2^14, 2^15), which makes bf16 exact (elements
+      // 2^38 below it aside)
+      cp_async_wait_all();
+      __syncwarp();
+      float c;
+      {
+        float mx = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < D / 8; ++k) {
+          const uint4 v = *reinterpret_cast<const uint4*>(qrow + (k >> 3) * (TA_ROWS * 128) + (((k & 7) ^ (rl & 7)) << 4));
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
-#pragma unroll
-          for (int o = 1; o < LANES; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          const int ex = query_exponent(mx);
-          float f = p.scale < 0.f ? -power_of_2(ex) : power_of_2(ex), cc = fabsf(p.scale) * power_of_2(-ex);
-          if (!(cc > 0.f)) {                                 // scores of 0
-            f = 0.f;
-            cc = 1.f;
-          }
+            mx = max3(mx, fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u)));
+        }
+        const int ex = query_exponent(mx);
+        float f = p.scale < 0.f ? -power_of_2(ex) : power_of_2(ex);
+        c = fabsf(p.scale) * power_of_2(-ex);
+        if (!(c > 0.f)) {                                    // scores of 0
+          f = 0.f;
+          c = 1.f;
+        }
+#pragma unroll 4
+        for (int k = 0; k < D / 8; ++k) {
+          uint4* at = reinterpret_cast<uint4*>(qrow + (k >> 3) * (TA_ROWS * 128) + (((k & 7) ^ (rl & 7)) << 4));
+          const uint4 v = *at;
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) w[e] = pack_h2(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
-          const int rw = 32 * warp + (k0 + k) * PER + lane / LANES, ch = lane % LANES;
-          *reinterpret_cast<uint4*>(sm + (ch >> 3) * (TA_ROWS * 128) + rw * 128 + (((ch & 7) ^ (rw & 7)) << 4)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
-          const float mine = __shfl_sync(0xffffffffu, cc, (lane % PER) * LANES);   // of row (k0 + k) PER + lane % PER
-          if (lane / PER == k0 + k) c = mine;
+          *at = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
       fence_async_shared();
@@ -272,6 +288,10 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
       for (int u = u_first; u < u_end; ++u, ++i) {
         wait2(TB_S, i);
         tc_fence_after();
+        if (u + 1 == u_end && after < end) {                 // the segment's last first product is done
+          next = following(sg, after);
+          copy_queries();
+        }
         const int4 bad = *reinterpret_cast<const int4*>(s_bad[i & 1]);
         poison |= (bad.x | bad.y | bad.z | bad.w) != 0;
         const uint32_t at = trow + (i & 1) * TA_UNIT;
@@ -339,18 +359,7 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
         tc_fence_before();
         arrive(bar + TB_P + (i & 1));
       }
-      // ---- the segment's end in this share; the next one's queries meanwhile
-      const long long after = pos + (u_end - u_first);
-      if (after < end) {
-        next = following(sg, after);
-        const int r = next.tile * TA_ROWS + rl;
-        if (r < next.n * p.G) {
-          const int tok = r / p.G, hq = next.h * p.G + r - tok * p.G;
-          const bf16* src = static_cast<const bf16*>(p.q) + (long long)(next.r0 + tok) * p.q_row + hq * p.q_head;
-#pragma unroll
-          for (int k = 0; k < D; k += 64) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(src + k));
-        }
-      }
+      // ---- the segment's end in this share
       wait2(TB_DONE, i - 1);
       tc_fence_after();
       const bool whole = u_first == 0 && u_end == sg.nu;
@@ -363,17 +372,21 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
         const bool sector = ((whole ? (uintptr_t)p.out : (uintptr_t)part) & 31) == 0;
         const size_t at = (size_t)(sg.r0 + tok) * p.Hq + hq;
 #pragma unroll 1
-        for (int q = 0; q < D; q += 16) {
-          float o[16];
-          ta_ld16(trow + TA_O + q, o);
+        for (int q = 0; q < D; q += 32) {
+          float o[32];
+          tc_ld32_issue(trow + TA_O + q, o);
+          tc_wait_ld();
           if (live && whole) {
-            uint32_t y[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
-            store32(static_cast<bf16*>(p.out) + at * D + q, y, sector);
-          } else if (live) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+              uint32_t y[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) y[k] = pack_bf16(o[16 * h + 2 * k] * inv, o[16 * h + 2 * k + 1] * inv);
+              store32(static_cast<bf16*>(p.out) + at * D + q + 16 * h, y, sector);
+            }
+          } else if (live) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
               uint32_t y[8];
 #pragma unroll
               for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(o[8 * h + k]);
