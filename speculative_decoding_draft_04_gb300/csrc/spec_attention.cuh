@@ -50,8 +50,9 @@ struct AttnSeg {
   bool bad;
 };
 
-// Units of request b over all heads and row tiles (0: nothing to do).
-template <int ROWS, int UNIT>
+// Units of request b over all heads and row tiles (0: nothing to do).  LEAD: what
+// a segment costs besides its units, counted as units ahead of them.
+template <int ROWS, int UNIT, int LEAD>
 __device__ __forceinline__ long long attn_work(const AttnParams& p, int b, int& n, int& r0, int& L, int& tiles,
                                                int& nu, bool& bad, bool& outside) {
   r0 = __ldg(p.row_ptr + b);
@@ -68,13 +69,13 @@ __device__ __forceinline__ long long attn_work(const AttnParams& p, int b, int& 
   bad = L < n || L > (1 << 30) || L > (long long)p.stride * p.P;
   tiles = (n * p.G + ROWS - 1) / ROWS;
   nu = bad ? 1 : (L + UNIT - 1) / UNIT;
-  return (long long)p.Hkv * tiles * nu;
+  return (long long)p.Hkv * tiles * (nu + LEAD);
 }
 
 // Units before each group of requests, by the first THREADS threads of a CTA
 // (whole warps; the caller synchronises them before and after): s_pre[THREADS + 1],
 // s_scan[THREADS / 32].  A group is ceil(B / THREADS) requests.
-template <int ROWS, int UNIT, int THREADS, class Sync>
+template <int ROWS, int UNIT, int THREADS, int LEAD = 0, class Sync>
 __device__ __forceinline__ long long attn_prefix(const AttnParams& p, long long* s_pre, long long* s_scan, Sync sync) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int items = (p.B + THREADS - 1) / THREADS;
@@ -85,7 +86,7 @@ __device__ __forceinline__ long long attn_prefix(const AttnParams& p, long long*
     if (b >= p.B) break;
     int n, r0, L, tiles, nu;
     bool bad, outside;
-    mine += attn_work<ROWS, UNIT>(p, b, n, r0, L, tiles, nu, bad, outside);
+    mine += attn_work<ROWS, UNIT, LEAD>(p, b, n, r0, L, tiles, nu, bad, outside);
     flag |= bad || outside;
   }
   long long v = mine;
@@ -108,8 +109,8 @@ __device__ __forceinline__ long long attn_prefix(const AttnParams& p, long long*
   return all;
 }
 
-// The segment that holds unit `pos` (below the total).
-template <int ROWS, int UNIT, int THREADS>
+// The segment that holds unit `pos` (below the total); LEAD more units to `u`.
+template <int ROWS, int UNIT, int THREADS, int LEAD = 0>
 __device__ __forceinline__ AttnSeg attn_locate(const AttnParams& p, const long long* s_pre, long long pos) {
   const int items = (p.B + THREADS - 1) / THREADS;
   int lo = 0, hi = THREADS;
@@ -122,15 +123,15 @@ __device__ __forceinline__ AttnSeg attn_locate(const AttnParams& p, const long l
   int tiles;
   for (int b = lo * items;; ++b) {
     bool outside;
-    const long long w = attn_work<ROWS, UNIT>(p, b, s.n, s.r0, s.L, tiles, s.nu, s.bad, outside);
+    const long long w = attn_work<ROWS, UNIT, LEAD>(p, b, s.n, s.r0, s.L, tiles, s.nu, s.bad, outside);
     if (left < w) {
       s.b = b;
       break;
     }
     left -= w;
   }
-  const long long seg = left / s.nu;
-  s.u = (int)(left - seg * s.nu);
+  const long long seg = left / (s.nu + LEAD);
+  s.u = (int)(left - seg * (s.nu + LEAD));
   s.h = (int)(seg / tiles);
   s.tile = (int)(seg - (long long)s.h * tiles);
   return s;
@@ -247,14 +248,14 @@ __device__ __forceinline__ int k_order(int t, int s) {
 
 // The segment after one that ended, whose first unit is `pos`: most often the
 // same request's.
-template <int ROWS, int UNIT, int THREADS>
+template <int ROWS, int UNIT, int THREADS, int LEAD = 0>
 __device__ __forceinline__ AttnSeg attn_next(const AttnParams& p, const long long* s_pre, const AttnSeg& seg, long long pos) {
   AttnSeg s = seg;
   s.u = 0;
   if (++s.tile * ROWS < s.n * p.G) return s;
   s.tile = 0;
   if (++s.h < p.Hkv) return s;
-  return attn_locate<ROWS, UNIT, THREADS>(p, s_pre, pos);
+  return attn_locate<ROWS, UNIT, THREADS, LEAD>(p, s_pre, pos);
 }
 
 // The power of two that takes mx into [2^14, 2^15) (at most 2^120; 2^15 for 0,

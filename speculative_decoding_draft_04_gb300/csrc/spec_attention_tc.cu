@@ -12,13 +12,23 @@
 //   warps 0-3   softmax: a thread holds one row, so its maximum and sum need no
 //               exchange (the same lazy maximum as the other kernels)
 //   warps 4-7   decode: codes requested a unit of 64 tokens ahead into registers,
-//               decoded into two buffers of 16-bit floats
+//               decoded into two buffers of 16-bit floats; keys' and values'
+//               buffers are taken and given back apart
 //   warp 8      issues the products, the next unit's first one ahead of this
 //               unit's second one
 //
 // Two CTAs an SM, each with half of the tensor memory, cover each other's waits.
 // The units are numbered and shared, and split segments joined, as in the
-// kernels of smaller tiles.
+// kernels of smaller tiles, but a segment counts four units more: beginning and
+// ending one (queries in, outputs out, an empty pipeline) takes as long as that,
+// and short requests' segments would otherwise meet in one CTA (trees of 100 rows
+// over 32 requests of 25 to 4096 tokens: 119 us, with the lead 85).
+//
+// Bound by the chain of waits of a unit (2900 cycles, two CTAs at a time: 1450 a
+// unit and SM, of which the products are about 500), not by issue slots (32 %
+// used) or memory (9 %).  At that rate 100 of 128 rows reach 0.36 PFLOP/s; the
+// 16-row tiles of mma.sync took 265 us for the same trees, decoding every token
+// seven times.
 #include <atomic>
 
 #include "spec_attention.cuh"
@@ -27,6 +37,7 @@ namespace spec {
 
 constexpr int TA_UNIT = 64;                                  // tokens
 constexpr int TA_ROWS = 128;
+constexpr int TA_LEAD = 4;                                   // units that beginning and ending a segment costs
 constexpr int TA_PREFIX = 256;                               // threads of the prefix sums
 constexpr int TA_THREADS = 9 * 32;
 constexpr uint32_t TA_COLS = 256;                            // two buffers of scores, outputs
@@ -42,7 +53,7 @@ struct TaLayout {
   static constexpr int PART = TA_ROWS * D + 2 * TA_ROWS;
 };
 
-enum { TB_KV = 0, TB_DONE = 2, TB_S = 4, TB_P = 6, TB_Q = 8, TB_BARS = 9 };
+enum { TB_K = 0, TB_V = 2, TB_S = 4, TB_P = 6, TB_DONE = 8, TB_Q = 10, TB_BARS = 11 };
 
 // Operand kinds: A, B 16-bit floats, D fp32, M = 128.
 template <int N>
@@ -150,6 +161,37 @@ __device__ __forceinline__ uint32_t seen_word(const AttnParams& p, int d, int li
   return __funnelshift_r(word(d >> 5), word((d >> 5) + 1), d & 31) & first(L - ctx - d);
 }
 
+// The segments of a CTA's share [pos, end), each with the units u .. u_end - 1 of
+// it that are the CTA's.  A share that ends inside a segment's lead has none of
+// its units, and one that begins there has it from its first unit on.
+struct TaWalk {
+  AttnSeg sg;
+  int u_end;
+  long long pos, end;
+  __device__ __forceinline__ TaWalk(const AttnParams& p, const long long* s_pre, long long begin, long long end_)
+      : pos(begin), end(end_) {
+    if (pos < end) {
+      sg = attn_locate<TA_ROWS, TA_UNIT, TA_PREFIX, TA_LEAD>(p, s_pre, pos);
+      pos -= sg.u;                                           // where the segment begins
+      sg.u = max(sg.u - TA_LEAD, 0);
+      cut();
+    }
+  }
+  __device__ __forceinline__ void cut() {
+    const long long units = end - pos - TA_LEAD;
+    u_end = units < sg.nu ? (int)units : sg.nu;
+    if (u_end <= sg.u) pos = end;
+  }
+  __device__ __forceinline__ bool done() const { return pos >= end; }
+  __device__ __forceinline__ void next(const AttnParams& p, const long long* s_pre) {
+    pos += TA_LEAD + sg.nu;
+    if (pos < end) {
+      sg = attn_next<TA_ROWS, TA_UNIT, TA_PREFIX, TA_LEAD>(p, s_pre, sg, pos);
+      cut();
+    }
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const __grid_constant__ AttnParams p) {
   using L = TaLayout<D>;
@@ -160,19 +202,20 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
   __shared__ long long s_scan[TA_PREFIX / 32];
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail;
-  __shared__ __align__(16) int s_bad[2][4];                                // a unit's pages outside the cache, a decode warp each
+  __shared__ __align__(16) int s_bad[4][4];                                // a unit's pages outside the cache, a decode warp each
   uint8_t* sm = align1k(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
     s_fail = 0;
-    const int counts[TB_BARS] = {4, 4, 1, 1, 1, 1, 4, 4, 4};
-    for (int i = 0; i < TB_BARS; ++i) mbar_init(bar + i, counts[i]);
+    const int counts[TB_BARS / 2 + 1] = {D / 32, D / 32, 1, 4, 1, 4};   // arriving warps
+    for (int i = 0; i < TB_BARS; ++i) mbar_init(bar + i, counts[i / 2]);
+    for (int i = 0; i < 16; ++i) s_bad[i >> 2][i & 3] = 0;
   }
   if (warp == 8) tc_alloc(&s_tmem, TA_COLS);
   if (tid < TA_PREFIX)
-    attn_prefix<TA_ROWS, TA_UNIT, TA_PREFIX>(p, s_pre, s_scan,
-                                             [] { asm volatile("barrier.cta.sync.aligned 3, 256;\n" ::: "memory"); });
+    attn_prefix<TA_ROWS, TA_UNIT, TA_PREFIX, TA_LEAD>(p, s_pre, s_scan,
+                                                      [] { asm volatile("barrier.cta.sync.aligned 3, 256;\n" ::: "memory"); });
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -203,30 +246,26 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
     if (lane == 0)
       asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(b)) : "memory");
   };
-  auto locate = [&](long long at) { return attn_locate<TA_ROWS, TA_UNIT, TA_PREFIX>(p, s_pre, at); };
-  auto following = [&](const AttnSeg& s, long long at) {
-    return attn_next<TA_ROWS, TA_UNIT, TA_PREFIX>(p, s_pre, s, at);
-  };
   AttnSplit split{0, -1, 0, 0, 0, 0, 0};
 
-  if (begin >= end) {
+  TaWalk walk(p, s_pre, begin, end);
+  if (walk.done()) {
   } else if (warp < 4) {
     // ------------------------------------------------ softmax
     const uint32_t trow = tmem + ((uint32_t)(32 * warp) << 16);
     uint32_t i = 0;
     const int rl = 32 * warp + lane;                         // this thread's row
     uint8_t* const qrow = sm + rl * 128;
-    AttnSeg next = locate(begin);
     int ntok = 0, nhq = 0;                                   // the row's new token and query head; < 0: none
-    // Copies the warp's queries of segment `next` to their place, D / 8 lanes a
+    // Copies the warp's queries of the walk's segment to their place, D / 8 lanes a
     // row: once the last products of the segment before have read that.
     auto copy_queries = [&]() {
       constexpr int LANES = D / 8, PER = 32 / LANES;         // rows an instruction
-      const int r = next.tile * TA_ROWS + rl;
-      const bool there = r < next.n * p.G;
+      const int r = walk.sg.tile * TA_ROWS + rl;
+      const bool there = r < walk.sg.n * p.G;
       ntok = there ? r / p.G : -1;
-      nhq = next.h * p.G + (there ? r - ntok * p.G : 0);
-      const long long off = there ? (long long)(next.r0 + ntok) * p.q_row + nhq * p.q_head : -1;
+      nhq = walk.sg.h * p.G + (there ? r - ntok * p.G : 0);
+      const long long off = there ? (long long)(walk.sg.r0 + ntok) * p.q_row + nhq * p.q_head : -1;
       const int ch = lane % LANES;
 #pragma unroll
       for (int k = 0; k < LANES; ++k) {
@@ -238,11 +277,10 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
       cp_async_commit();
     };
     copy_queries();
-    for (long long pos = begin; pos < end;) {
-      const AttnSeg sg = next;
-      const int u_first = sg.u;
-      const int u_end = sg.nu - sg.u < end - pos ? sg.nu : sg.u + (int)(end - pos);
-      const long long after = pos + (u_end - u_first);
+    for (bool more = true; more;) {
+      const AttnSeg sg = walk.sg;
+      const int u_first = sg.u, u_end = walk.u_end;
+      const long long last = walk.pos + TA_LEAD + sg.nu - 1;   // the segment's last unit
       const int ctx = sg.L - sg.n;
       const bool live = ntok >= 0;
       const int tok = live ? ntok : 0, hq = nhq;
@@ -288,11 +326,12 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
       for (int u = u_first; u < u_end; ++u, ++i) {
         wait2(TB_S, i);
         tc_fence_after();
-        if (u + 1 == u_end && after < end) {                 // the segment's last first product is done
-          next = following(sg, after);
-          copy_queries();
+        if (u + 1 == u_end) {                                // the segment's last first product is done
+          walk.next(p, s_pre);
+          more = !walk.done();
+          if (more) copy_queries();
         }
-        const int4 bad = *reinterpret_cast<const int4*>(s_bad[i & 1]);
+        const int4 bad = *reinterpret_cast<const int4*>(s_bad[i & 3]);
         poison |= (bad.x | bad.y | bad.z | bad.w) != 0;
         const uint32_t at = trow + (i & 1) * TA_UNIT;
         if (some) {
@@ -399,8 +438,7 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
       }
       tc_fence_before();                                     // before the next segment's first P
       if (!whole && slot == 1)
-        split = AttnSplit{me, (int)((pos + (sg.nu - 1)) / share), sg.b, sg.h, sg.tile, sg.n, sg.r0};
-      pos = after;
+        split = AttnSplit{me, (int)(last / share), sg.b, sg.h, sg.tile, sg.n, sg.r0};
     }
   } else if (warp < 8) {
     // ------------------------------------------------ decode
@@ -408,11 +446,11 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
     // of one of them
     const int w = tid - 128, tok = w & 63;
     const int bpp = p.P / CACHE_BLOCK, page_bits = 31 - __clz(p.P);
-    AttnSeg ps = locate(begin);
-    long long pos = begin;                                   // the unit to request next
-    int page;                                           // its page of that unit
+    const AttnSeg& ps = walk.sg;
+    int u = ps.u;                                            // the unit to request next
+    int page;                                                // its page of that unit
     auto pages = [&]() {
-      const int at = ps.bad ? 0 : min(ps.u * TA_UNIT + tok, ps.L - 1);
+      const int at = ps.bad ? 0 : min(u * TA_UNIT + tok, ps.L - 1);
       page = (int)load_now(reinterpret_cast<const uint32_t*>(p.table) + (size_t)ps.b * p.stride + (at >> page_bits));
     };
     struct Codes {
@@ -426,7 +464,7 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
     // no branch around the loads, and none that keeps a value instead: what is
     // loaded stays in flight until it is decoded (past the end: the last unit again)
     auto request = [&](Codes& x) {
-      const int at = ps.u * TA_UNIT + tok;
+      const int at = u * TA_UNIT + tok;
       x.there = at < ps.L;
       x.bad = x.there && (uint32_t)page >= (uint32_t)p.num_pages;
       const uint8_t* blk = p.cache + (size_t)ps.h * head_bytes +
@@ -440,63 +478,70 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
         x.scale[k] = load_now(reinterpret_cast<const uint32_t*>(blk + (is_v(k) ? cache_v_scales(D) : cache_k_scales(D)) +
                                                                 (tok & 15) * (D / 16) + half * 4));
       }
-      if (pos + 1 < end) {
-        ++pos;
-        if (++ps.u >= ps.nu) ps = following(ps, pos);
+      if (u + 1 < walk.u_end) {
+        ++u;
+      } else {
+        walk.next(p, s_pre);
+        if (!walk.done()) u = ps.u; else walk.pos = end;
       }
       pages();
     };
-    auto unit = [&](uint32_t i, const Codes& x) {
-      if (i >= 2) wait2(TB_DONE, i - 2);                     // the products that read this buffer
+    auto spread = [&](uint8_t* half0, const uint4 (&code)[2], uint32_t scale) {
+      uint8_t* dst = half0 + half * (TA_UNIT * 128) + tok * 128;
 #pragma unroll
-      for (int k = 0; k < TASKS; ++k) {
-        uint8_t* dst = sm + (is_v(k) ? L::V : L::K) + (i & 1) * L::HALF + half * (TA_UNIT * 128) + tok * 128;
-        // tokens that nobody wrote: values of 0
-        const bool zero = is_v(k) && !x.there;
-        const uint32_t scale = zero ? 0u : x.scale[k];
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t two = decode_scales(scale >> (16 * q));
+        const uint32_t f[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
+        const uint32_t c[4] = {code[q].x, code[q].y, code[q].z, code[q].w};
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint32_t two = decode_scales(scale >> (16 * q));
-          const uint32_t f[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
-          const uint4 v = x.code[k][q];
-          const uint32_t c[4] = {v.x, v.y, v.z, v.w};
+        for (int j = 0; j < 4; ++j) {
+          uint32_t h[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t h[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = mul_h2(decode_byte(c, 4 * j + e), f[j >> 1]);
-            *reinterpret_cast<uint4*>(dst + (((4 * q + j) ^ (tok & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-          }
+          for (int e = 0; e < 4; ++e) h[e] = mul_h2(decode_byte(c, 4 * j + e), f[j >> 1]);
+          *reinterpret_cast<uint4*>(dst + (((4 * q + j) ^ (tok & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
         }
       }
-      const bool bad = __any_sync(0xffffffffu, x.bad);
-      if (lane == 0) {
-        s_bad[i & 1][warp & 3] = bad;
-        if (bad) set_status(p.status, SPEC_DEV_BAD_SLOT);
-      }
       fence_async_shared();
-      arrive(bar + TB_KV + (i & 1));
+    };
+    auto unit = [&](uint32_t i, const Codes& x) {
+      // keys: their buffer is free once the first product of two units ago is done
+      if (D == 128 || w < 64) {
+        const bool bad = __any_sync(0xffffffffu, x.bad);
+        if (i >= 2) wait2(TB_S, i - 2);
+        if (lane == 0) {
+          s_bad[i & 3][warp & 3] = bad;
+          if (bad) set_status(p.status, SPEC_DEV_BAD_SLOT);
+        }
+        spread(sm + L::K + (i & 1) * L::HALF, x.code[0], x.scale[0]);
+        arrive(bar + TB_K + (i & 1));
+      }
+      // values: once the second one is; 0 for tokens that nobody wrote
+      if (D == 128 || w >= 64) {
+        if (i >= 2) wait2(TB_DONE, i - 2);
+        uint4 code[2] = {x.code[TASKS - 1][0], x.code[TASKS - 1][1]};
+        spread(sm + L::V + (i & 1) * L::HALF, code, x.there ? x.scale[TASKS - 1] : 0u);
+        arrive(bar + TB_V + (i & 1));
+      }
     };
     pages();
     request(even);
-    const uint32_t n = (uint32_t)(end - begin);
-    for (uint32_t i = 0; i < n; i += 2) {
+    for (uint32_t i = 0;; i += 2) {
+      const bool last = walk.done();
       request(odds);
       unit(i, even);
-      if (i + 1 < n) {
-        request(even);
-        unit(i + 1, odds);
-      }
+      if (last) break;
+      const bool last2 = walk.done();
+      request(even);
+      unit(i + 1, odds);
+      if (last2) break;
     }
   } else {
     // ------------------------------------------------ products
     const uint32_t el = ta_elect();
     const uint32_t q0 = smem_u32(sm), k0 = q0 + L::K, v0 = q0 + L::V;
-    AttnSeg sg = locate(begin);
-    const uint32_t n = (uint32_t)(end - begin);
-    uint32_t segs = 0, seg_end = 0;                          // first unit after the segment
     bool first_prev = false;
     auto second = [&](uint32_t i, bool first) {
+      wait2(TB_V, i);
       wait2(TB_P, i);
       tc_fence_after();
 #pragma unroll
@@ -505,30 +550,27 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
                   tc_sdesc(v0 + (i & 1) * L::HALF + k * 2048, TA_UNIT * 128, 1024), ta_idesc<D>(1), first && k == 0 ? 0u : 1u);
       ta_commit(el, bar + TB_DONE + (i & 1));
     };
-    for (uint32_t i = 0; i < n; ++i) {
-      const bool first = i == seg_end;
-      if (first) {
-        if (i > 0) {
-          second(i - 1, first_prev);                         // the softmax warps end the segment after it
-          sg = following(sg, begin + i);
+    uint32_t i = 0;
+    for (uint32_t segs = 0; !walk.done(); walk.next(p, s_pre), ++segs)
+      for (int u = walk.sg.u; u < walk.u_end; ++u, ++i) {
+        const bool first = u == walk.sg.u;
+        if (first) {
+          if (i > 0) second(i - 1, first_prev);              // the softmax warps end the segment after it
+          wait(bar + TB_Q, segs & 1);
         }
-        seg_end = i + (uint32_t)(sg.nu - sg.u);
-        wait(bar + TB_Q, segs & 1);
-        ++segs;
-      }
-      wait2(TB_KV, i);
-      tc_fence_after();
+        wait2(TB_K, i);
+        tc_fence_after();
 #pragma unroll
-      for (int s = 0; s < KSTEPS; ++s)
-        ta_mma_ss(el, tmem + (i & 1) * TA_UNIT, tc_sdesc(q0 + (s >> 2) * (TA_ROWS * 128) + (s & 3) * 32, 16, 1024),
-                  tc_sdesc(k0 + (i & 1) * L::HALF + (s >> 2) * (TA_UNIT * 128) + (s & 3) * 32, 16, 1024), ta_idesc<TA_UNIT>(0),
-                  s > 0 ? 1u : 0u);
-      ta_commit(el, bar + TB_S + (i & 1));
-      if (!first) second(i - 1, first_prev);
-      first_prev = first;
-    }
-    second(n - 1, first_prev);
-    wait2(TB_DONE, n - 1);                                   // nothing in flight when tensor memory goes
+        for (int s = 0; s < KSTEPS; ++s)
+          ta_mma_ss(el, tmem + (i & 1) * TA_UNIT, tc_sdesc(q0 + (s >> 2) * (TA_ROWS * 128) + (s & 3) * 32, 16, 1024),
+                    tc_sdesc(k0 + (i & 1) * L::HALF + (s >> 2) * (TA_UNIT * 128) + (s & 3) * 32, 16, 1024), ta_idesc<TA_UNIT>(0),
+                    s > 0 ? 1u : 0u);
+        ta_commit(el, bar + TB_S + (i & 1));
+        if (!first) second(i - 1, first_prev);
+        first_prev = first;
+      }
+    second(i - 1, first_prev);
+    wait2(TB_DONE, i - 1);                                   // nothing in flight when tensor memory goes
   }
   tc_fence_before();
   __syncthreads();
