@@ -271,11 +271,14 @@ __device__ __forceinline__ float power_of_2(int e) { return __uint_as_float((uin
 cudaError_t launch_cache_attention_tc(const AttnParams& p, int D, int sms, cudaStream_t st);
 
 // Adds the parts of the split segments: CTA (x, y) takes the segments that
-// begin at workers x, x + gridDim.x, .. and JOIN_ROWS rows of each.  A part is
+// begin at workers x, x + gridDim.x, .. and 1024 / D rows of each.  A part is
 // [ROWS][D] unnormalised outputs and (m, sum) a row; worker w has slot 0 for a
 // segment that began before its share and slot 1 for one that begins in it.
-// Threads that the rows leave over share the parts; the order of every sum
-// depends on the numbers of rows and parts alone.
+// Threads that the rows leave over share the parts, and each requests JOIN_BATCH
+// of them before it adds the first, so a long context's 30 parts cost a few round
+// trips; the order of every sum depends on the numbers of rows and parts alone.
+// Its launch overlaps the main kernel's end; 10 to 25 us by itself with cold
+// caches (two rows a CTA: 24 us where 14 are kept, for 1824 workers of 2 parts).
 constexpr int JOIN_THREADS = 256, JOIN_BATCH = 4;
 template <int D, int ROWS, class DT>
 __global__ void __launch_bounds__(JOIN_THREADS) cache_attention_join_kernel(const __grid_constant__ AttnParams p, int workers) {

@@ -14,6 +14,12 @@
 // collected and ranked by counting.  Equal values beyond the list's size (a
 // row of few different values) are found one by one instead.
 //
+// Bound by latency between its phases (load, maxima, sums, bound, candidates), not
+// by bytes: 128 requests of 1 to 8 tokens and 32000 bf16 logits (37 MB) take
+// 20 us, 256 of 128256 (296 MB) 92 us, 3.2 TB/s of the 6.8 of a copy.  Two CTAs of
+// 64 KB in registers an SM overlap each other's phases; half the vectors and four
+// CTAs took 27 and 90 us (rows of two segments to join), three CTAs spilled.
+//
 // Rows of more than one segment are joined by logprobs_join_kernel, a warp a
 // row, from each segment's (m, Z, sum 2^d d) and its K sorted candidates; its
 // launch overlaps the first kernel's end.
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(LP_THREADS, 2) logprobs_kernel(const __grid_co
 #pragma unroll
     for (int j = 0; j < LP_VECS; ++j) hit |= (vm[j] >= bound ? 1u : 0u) << j;
     // few vectors: read again rather than picked out of the registers, which
-    // would take the code of all eight (it is bound by instruction fetches then)
+    // would take the code of every vector (it is bound by instruction fetches then)
     while (hit) {
       const int j = __ffs(hit) - 1, at = (i0 + j * LP_THREADS) * E - lead;
       hit &= hit - 1;
