@@ -455,9 +455,9 @@ def spec_tree_verify(target, U, W1, W2, anchor, temperature, parent, mask, token
 
 # ------------------------------------------------------- target side of a cycle
 # These calls are made every step of a server, some of them for microseconds of
-# GPU work: their arguments are packed into the C structs' bytes in one go (the
-# formats follow the structures above field by field), and checked by identity
-# and tuple comparison.
+# GPU work: their tensors are checked by the compiled module _args, and their
+# arguments packed into the C structs' bytes in one go (the formats follow the
+# structures above field by field).
 
 def _format(py) -> struct.Struct:
     """struct format of a mirror, native alignment."""
@@ -467,42 +467,29 @@ def _format(py) -> struct.Struct:
 
 _TABLES, _APPEND = _format(BlockTablesArgs), _format(CacheAppendArgs)
 _ATTENTION, _LOGPROBS = _format(CacheAttentionArgs), _format(LogprobsArgs)
-_torch = None
+_torch = _args = None
 
 
 def _types():
-    """torch, imported at the first call that needs it."""
-    global _torch
+    """torch, imported at the first call that needs it, with the module that
+    checks tensors."""
+    global _torch, _args
     if _torch is None:
         import torch
-        _torch = torch
+        try:
+            from . import _args as checks
+        except ImportError as e:
+            raise SpecError(f"the compiled checks are missing ({e}): build them with "
+                            "speculative_decoding_draft_04_gb300.build.build()") from e
+        checks.use(SpecError)
+        _torch, _args = torch, checks
     return _torch
 
 
 def _raw_stream(stream) -> int:
     if stream is not None:
         return stream.cuda_stream
-    return _torch._C._cuda_getCurrentRawStream(_torch.cuda.current_device())
-
-
-def _tensor(t, what: str, dtype, shape: tuple) -> int:
-    """Address of a contiguous CUDA tensor of this type and shape."""
-    if t.dtype is not dtype or t.shape != shape:
-        raise SpecError(f"{what} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
-    if not (t.is_cuda and t.is_contiguous()):
-        raise SpecError(f"{what} must be a contiguous CUDA tensor")
-    return t.data_ptr()
-
-
-def _heads(t, what: str, shape: tuple) -> tuple:
-    """Address, row and head stride of a CUDA tensor [T][H][D] whose heads are contiguous."""
-    s = t.stride()
-    if t.shape != shape or s[2] != 1:
-        raise SpecError(f"{what} must be {list(shape)} with contiguous heads, not {list(t.shape)} "
-                        f"with strides {list(s)}")
-    if not t.is_cuda:
-        raise SpecError(f"{what} must be a CUDA tensor")
-    return t.data_ptr(), s[0], s[1]
+    return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
 
 
 def _cache_shape(cache, D: int) -> tuple:
@@ -537,16 +524,13 @@ def spec_block_tables(seq_len, accept_len, new_len, num_blocks, ring_pos, free_r
     B, table, rows, ring = b[0], tuple(block_table.shape), tuple(slots.shape), tuple(free_ring.shape)
     if len(b) != 1 or len(table) != 2 or len(rows) != 1 or len(ring) != 1 or table[0] != B:
         raise SpecError("seq_len, slots and free_ring must be vectors, block_table [B, pages]")
-    a = _TABLES.pack(
-        B, page_size, ring[0], table[1], rows[0], _tensor(seq_len, "seq_len", i32, b),
-        0 if accept_len is None else _tensor(accept_len, "accept_len", i32, b),
-        _tensor(new_len, "new_len", i32, b), _tensor(num_blocks, "num_blocks", i32, b),
-        _tensor(ring_pos, "ring_pos", i64, (2,)), _tensor(free_ring, "free_ring", i32, ring),
-        _tensor(block_table, "block_table", i32, table), _tensor(seq_len_out, "seq_len_out", i32, b),
-        _tensor(kv_len, "kv_len", i32, b), _tensor(num_blocks_out, "num_blocks_out", i32, b),
-        _tensor(ring_pos_out, "ring_pos_out", i64, (2,)), _tensor(row_ptr, "row_ptr", i32, (B + 1,)),
-        _tensor(slots, "slots", i32, rows), _tensor(positions, "positions", i32, rows),
-        _tensor(dev_status, "dev_status", i32, (4,)))
+    a = _TABLES.pack(B, page_size, ring[0], table[1], rows[0], *_args.addresses(
+        "seq_len", seq_len, i32, b, "accept_len?", accept_len, i32, b, "new_len", new_len, i32, b,
+        "num_blocks", num_blocks, i32, b, "ring_pos", ring_pos, i64, (2,), "free_ring", free_ring, i32, ring,
+        "block_table", block_table, i32, table, "seq_len_out", seq_len_out, i32, b, "kv_len", kv_len, i32, b,
+        "num_blocks_out", num_blocks_out, i32, b, "ring_pos_out", ring_pos_out, i64, (2,),
+        "row_ptr", row_ptr, i32, (B + 1,), "slots", slots, i32, rows, "positions", positions, i32, rows,
+        "dev_status", dev_status, i32, (4,)))
     rc = lib().spec_block_tables(a, _raw_stream(stream))
     if rc:
         _check(rc, "spec_block_tables")
@@ -564,14 +548,12 @@ def spec_cache_append(k, v, slots, cache, dev_status, k_scale: float = 1.0, v_sc
     pages, Hkv, P = _cache_shape(cache, D)
     if Hkv != H or v.dtype is not k.dtype:
         raise SpecError(f"k, v and cache disagree: {H} and {Hkv} heads, {k.dtype} and {v.dtype}")
-    kp, kr, kh = _heads(k, "k", shape)
-    vp, vr, vh = _heads(v, "v", shape)
-    a = _APPEND.pack(
-        rows, H, D, _storage(k), P, pages, kp, vp, kr, kh, vr, vh, _tensor(slots, "slots", T.int32, (rows,)),
-        k_scale, v_scale, _tensor(cache, "cache", T.uint8, cache.shape),
-        0 if k_stored is None else _tensor(k_stored, "k_stored", k.dtype, shape),
-        0 if v_stored is None else _tensor(v_stored, "v_stored", k.dtype, shape),
-        _tensor(dev_status, "dev_status", T.int32, (4,)))
+    kp, kr, kh, vp, vr, vh, sp, cp, ks, vs, st = _args.addresses(
+        "k", k, None, shape, "v", v, None, shape, "slots", slots, T.int32, (rows,),
+        "cache", cache, T.uint8, (pages, H, P // 16, 18 * D), "k_stored?", k_stored, k.dtype, shape,
+        "v_stored?", v_stored, k.dtype, shape, "dev_status", dev_status, T.int32, (4,))
+    a = _APPEND.pack(rows, H, D, _storage(k), P, pages, kp, vp, kr, kh, vr, vh, sp, k_scale, v_scale, cp,
+                     ks, vs, st)
     rc = lib().spec_cache_append(a, _raw_stream(stream))
     if rc:
         _check(rc, "spec_cache_append")
@@ -596,15 +578,14 @@ def spec_cache_attention(q, cache, block_table, kv_len, row_ptr, out, dev_status
     B = table[0]
     pages, Hkv, P = _cache_shape(cache, D)
     words = 0 if tree_mask is None else tree_mask.shape[1]
-    qp, qr, qh = _heads(q, "q", shape)
+    qp, qr, qh, cp, tp, lp, rp, mp, op, ep, st = _args.addresses(
+        "q", q, None, shape, "cache", cache, T.uint8, (pages, Hkv, P // 16, 18 * D),
+        "block_table", block_table, i32, table, "kv_len", kv_len, i32, (B,), "row_ptr", row_ptr, i32, (B + 1,),
+        "tree_mask?", tree_mask, i32, (rows, words), "out", out, q.dtype, shape, "lse?", lse, T.float32, (rows, Hq),
+        "dev_status", dev_status, i32, (4,))
     a = _ATTENTION.pack(
-        B, rows, Hq, Hkv, D, _storage(q), P, pages, table[1], words, qp, qr, qh,
-        _tensor(cache, "cache", T.uint8, cache.shape), _tensor(block_table, "block_table", i32, table),
-        _tensor(kv_len, "kv_len", i32, (B,)), _tensor(row_ptr, "row_ptr", i32, (B + 1,)),
-        0 if tree_mask is None else _tensor(tree_mask, "tree_mask", i32, (rows, words)),
-        softmax_scale, k_scale, v_scale, _tensor(out, "out", q.dtype, shape),
-        0 if lse is None else _tensor(lse, "lse", T.float32, (rows, Hq)),
-        _tensor(dev_status, "dev_status", i32, (4,)), _ptr(workspace), workspace.nbytes)
+        B, rows, Hq, Hkv, D, _storage(q), P, pages, table[1], words, qp, qr, qh, cp, tp, lp, rp, mp,
+        softmax_scale, k_scale, v_scale, op, ep, st, _ptr(workspace), workspace.nbytes)
     rc = lib().spec_cache_attention(a, _raw_stream(stream))
     if rc:
         _check(rc, "spec_cache_attention")
@@ -627,13 +608,13 @@ def spec_logprobs(logits, tokens, logprob, entropy, dev_status, workspace, tempe
         raise SpecError("top_ids and top_logprobs go together")
     B, n, V = shape
     K = 0 if top_ids is None else top_ids.shape[2]
+    tp, Tp, lp, ep, ip, kp, st = _args.addresses(
+        "tokens", tokens, i32, (B, n), "temperature?", temperature, f32, (B,), "logprob", logprob, f32, (B, n),
+        "entropy", entropy, f32, (B, n), "top_ids?", top_ids, i32, (B, n, K),
+        "top_logprobs?", top_logprobs, f32, (B, n, K), "dev_status", dev_status, i32, (4,))
     a = _LOGPROBS.pack(
-        B, n, V, K, _storage(logits), logits.data_ptr(), s[0], s[1], _tensor(tokens, "tokens", i32, (B, n)),
-        0 if temperature is None else _tensor(temperature, "temperature", f32, (B,)),
-        _tensor(logprob, "logprob", f32, (B, n)), _tensor(entropy, "entropy", f32, (B, n)),
-        _tensor(top_ids, "top_ids", i32, (B, n, K)) if K else 0,
-        _tensor(top_logprobs, "top_logprobs", f32, (B, n, K)) if K else 0,
-        _tensor(dev_status, "dev_status", i32, (4,)), _ptr(workspace), workspace.nbytes)
+        B, n, V, K, _storage(logits), logits.data_ptr(), s[0], s[1], tp, Tp, lp, ep, ip if K else 0,
+        kp if K else 0, st, _ptr(workspace), workspace.nbytes)
     rc = lib().spec_logprobs(a, _raw_stream(stream))
     if rc:
         _check(rc, "spec_logprobs")

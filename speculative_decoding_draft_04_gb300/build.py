@@ -2,8 +2,9 @@
 
 Each CUDA translation unit is compiled in parallel with nvcc and linked into
 ``libspec.so`` next to this file.  The CUDA runtime is linked statically, so
-the library only needs the driver at run time.  Rebuilds only when a source
-or header is newer than the library.
+the library only needs the driver at run time.  Beside it, the binding's checks
+of tensor arguments are compiled into the Python module ``_args``.  Rebuilds only
+when a source or header is newer than either.
 """
 from __future__ import annotations
 
@@ -11,12 +12,14 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libspec.so")
+ARGS = os.path.join(HERE, "_args.so")
 SOURCES = ["spec_abi.cu", "spec_draft.cu", "spec_draft_slice.cu", "spec_verify.cu",
            "spec_verify_slice.cu", "spec_verify_redecide.cu", "spec_refine.cu", "spec_report.cu",
            "spec_sched.cu", "spec_tree.cu", "spec_tables.cu", "spec_cache.cu", "spec_attention.cu", "spec_attention_tc.cu",
@@ -34,20 +37,37 @@ def _nvcc() -> str:
 
 
 def _inputs() -> list[str]:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh"))]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".cpp"))]
     files.append(os.path.join(INCLUDE, "spec.h"))
     return files
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(ARGS)):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(ARGS))
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
+def _build_args() -> None:
+    import torch
+    home = os.path.dirname(torch.__file__)
+    inc = os.path.join(home, "include")
+    tmp = ARGS + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I" + sysconfig.get_paths()["include"], "-I" + inc,
+           "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
+           os.path.join(CSRC, "spec_args.cpp"), "-o", tmp, "-L" + os.path.join(home, "lib"),
+           "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on spec_args.cpp:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, ARGS)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libspec.so; returns its path."""
+    """Compile and link libspec.so and _args.so; returns the library's path."""
     if not force and not is_stale():
         return LIB
     nvcc = _nvcc()
@@ -63,8 +83,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(res.stdout + res.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        args = ex.submit(_build_args)
         objs = list(ex.map(compile_one, SOURCES))
+        args.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)

@@ -1,0 +1,104 @@
+// The binding's checks of tensor arguments (Python module _args): a call of
+// microseconds of GPU work has up to fifteen tensors, and looking at one from
+// Python takes 0.33 us (five attribute reads), here 0.03.
+//
+//   use(error)                      the exception that refusals raise
+//   addresses(what, t, dtype, shape, ...)  four arguments a tensor; the addresses
+//       of contiguous CUDA tensors of these types and shapes.  dtype None: heads
+//       contiguous, any dtype; address, row stride, head stride of [T][H][D].
+//       t None: 0 where `what` ends in '?', else refused.
+#include <c10/core/ScalarType.h>
+#include <torch/csrc/Dtype.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <string>
+
+namespace {
+
+PyObject* g_error = nullptr;
+
+std::string list_of(c10::IntArrayRef x) {
+  std::string s = "[";
+  for (size_t i = 0; i < x.size(); ++i) s += (i ? ", " : "") + std::to_string(x[i]);
+  return s + "]";
+}
+std::string text(PyObject* o) {
+  PyObject* s = PyObject_Str(o);
+  const char* c = s ? PyUnicode_AsUTF8(s) : nullptr;
+  const std::string r = c ? c : "?";
+  Py_XDECREF(s);
+  if (!c) PyErr_Clear();
+  return r;
+}
+PyObject* refuse(const std::string& message) {
+  PyErr_SetString(g_error ? g_error : PyExc_RuntimeError, message.c_str());
+  return nullptr;
+}
+bool same_shape(c10::IntArrayRef have, PyObject* want) {
+  if (!PyTuple_Check(want) || PyTuple_GET_SIZE(want) != (Py_ssize_t)have.size()) return false;
+  for (size_t i = 0; i < have.size(); ++i) {
+    const long long n = PyLong_AsLongLong(PyTuple_GET_ITEM(want, i));
+    if (n != have[i]) {
+      PyErr_Clear();
+      return false;
+    }
+  }
+  return true;
+}
+
+PyObject* use(PyObject*, PyObject* error) {
+  Py_INCREF(error);
+  Py_XDECREF(g_error);
+  g_error = error;
+  Py_RETURN_NONE;
+}
+
+PyObject* addresses(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  constexpr Py_ssize_t MOST = 64;
+  long long out[MOST];
+  Py_ssize_t m = 0;
+  if (n % 4 != 0) return refuse("four arguments a tensor");
+  for (Py_ssize_t i = 0; i < n; i += 4) {
+    if (m + 3 > MOST) return refuse("too many tensors");
+    PyObject *what = a[i], *t = a[i + 1], *dtype = a[i + 2], *shape = a[i + 3];
+    if (t == Py_None) {
+      const std::string name = text(what);
+      if (name.empty() || name.back() != '?') return refuse(name + " is missing");
+      out[m++] = 0;
+      continue;
+    }
+    if (!THPVariable_Check(t)) return refuse(text(what) + " must be a tensor");
+    const at::Tensor& x = THPVariable_Unpack(t);
+    if (dtype == Py_None) {
+      if (!same_shape(x.sizes(), shape) || x.dim() != 3 || x.stride(2) != 1)
+        return refuse(text(what) + " must be " + text(shape) + " with contiguous heads, not " + list_of(x.sizes()) +
+                      " with strides " + list_of(x.strides()));
+      if (!x.is_cuda()) return refuse(text(what) + " must be a CUDA tensor");
+      out[m++] = (long long)(uintptr_t)x.data_ptr();
+      out[m++] = x.stride(0);
+      out[m++] = x.stride(1);
+      continue;
+    }
+    if (!THPDtype_Check(dtype)) return refuse("a dtype is expected for " + text(what));
+    if (x.scalar_type() != reinterpret_cast<THPDtype*>(dtype)->scalar_type || !same_shape(x.sizes(), shape))
+      return refuse(text(what) + " must be " + text(dtype) + " " + text(shape) + ", not " + c10::toString(x.scalar_type()) +
+                    " " + list_of(x.sizes()));
+    if (!x.is_cuda() || !x.is_contiguous()) return refuse(text(what) + " must be a contiguous CUDA tensor");
+    out[m++] = (long long)(uintptr_t)x.data_ptr();
+  }
+  PyObject* r = PyTuple_New(m);
+  if (!r) return nullptr;
+  for (Py_ssize_t i = 0; i < m; ++i) PyTuple_SET_ITEM(r, i, PyLong_FromLongLong(out[i]));
+  return r;
+}
+
+PyMethodDef methods[] = {
+    {"use", use, METH_O, "The exception that refusals raise."},
+    {"addresses", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(addresses)), METH_FASTCALL,
+     "Checked addresses (and strides) of tensors."},
+    {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_args", "Checks of tensor arguments.", -1, methods};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__args() { return PyModule_Create(&module); }
