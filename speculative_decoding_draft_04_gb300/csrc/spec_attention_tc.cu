@@ -22,13 +22,13 @@
 // kernels of smaller tiles, but a segment counts four units more: beginning and
 // ending one (queries in, outputs out, an empty pipeline) takes as long as that,
 // and short requests' segments would otherwise meet in one CTA (trees of 100 rows
-// over 32 requests of 25 to 4096 tokens: 119 us, with the lead 85).
+// over 32 requests of 25 to 4096 tokens: 119 us, with the lead 85, cold caches).
 //
-// Bound by the chain of waits of a unit (2900 cycles, two CTAs at a time: 1450 a
-// unit and SM, of which the products are about 500), not by issue slots (32 %
-// used) or memory (9 %).  At that rate 100 of 128 rows reach 0.36 PFLOP/s; the
-// 16-row tiles of mma.sync took 265 us for the same trees, decoding every token
-// seven times.
+// Bound by the chain of waits from step to step of a unit: 3500 cycles a unit
+// and CTA, two CTAs at a time, of which the products are some 500 a unit.  The
+// trees keep 42 % of the issue slots, 27 % of the tensor pipe and 19 % of the
+// memory busy.  100 of 128 rows reach 0.4 PFLOP/s (75 us a call); 16-row tiles of
+// mma.sync took 265 us for the same trees, decoding every token seven times.
 #include <atomic>
 
 #include "spec_attention.cuh"

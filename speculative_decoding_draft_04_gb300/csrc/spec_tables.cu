@@ -16,7 +16,7 @@
 // call does not write, so no thread waits for another's store.
 //
 // Bound by latency: lengths, then ring and table entries, then stores, 6.8 us in
-// a graph for 128 requests of 8 rows (10.4 us a call from Python; its bytes are
+// a graph for 128 requests of 8 rows (8.2 us a call from Python; its bytes are
 // 10 KB).  2048 prompts with a million rows (17 MB, 2.5 us of copying) take
 // 16 us: the rows' bisections, 11 steps each in shared memory.
 #include "spec_serve.cuh"
