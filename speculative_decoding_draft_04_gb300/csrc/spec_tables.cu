@@ -15,16 +15,17 @@
 // taken are read from the ring and pages kept from the table entries that the
 // call does not write, so no thread waits for another's store.
 //
-// Bound by latency: lengths, then ring and table entries, then stores, 6.8 us in
+// Bound by latency: lengths, then ring and table entries, then stores, 6.3 us in
 // a graph for 128 requests of 8 rows (8.2 us a call from Python; its bytes are
 // 10 KB).  2048 prompts with a million rows (17 MB, 2.5 us of copying) take
-// 16 us: the rows' bisections, 11 steps each in shared memory.
+// 13.7 us: instructions, the rows' bisections of 11 steps each in shared memory
+// (16.4 us with divisions by the page size and a loop over the warps' sums).
 #include "spec_serve.cuh"
 
 namespace spec {
 
 struct TablesParams {
-  int B, P, num_pages, stride, max_rows;
+  int B, P, page_bits, num_pages, stride, max_rows;
   const int* seq_len;
   const int* accept_len;
   const int* new_len;
@@ -56,7 +57,7 @@ __device__ __forceinline__ TablesRequest tables_request(const TablesParams& p, i
   TablesRequest r;
   r.held = held;
   bad = seq < 0 || acc < -1 || add < -1 || held < 0 || held > p.stride || kv > (long long)p.stride * p.P ||
-        kv > 0x3fffffff || (base + p.P - 1) / p.P > held;
+        kv > 0x3fffffff || ((base + p.P - 1) >> p.page_bits) > held;
   if (bad) {
     r.base = seq;
     r.add = 0;
@@ -64,31 +65,38 @@ __device__ __forceinline__ TablesRequest tables_request(const TablesParams& p, i
   } else {
     r.base = (int)base;
     r.add = add > 0 ? add : 0;
-    r.need = (int)((kv + p.P - 1) / p.P);
+    r.need = (int)((kv + p.P - 1) >> p.page_bits);
   }
   return r;
 }
 
-// Inclusive scan over the CTA of one value a thread; total over the CTA.
-__device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long* s_warp,
-                                                         unsigned long long& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+// Inclusive scans over the CTA of two values a thread; totals over the CTA.
+struct Two {
+  unsigned long long pages, rows;
+};
+__device__ __forceinline__ Two warp_scan(Two v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
+    const unsigned long long a = __shfl_up_sync(0xffffffffu, v.pages, o), b = __shfl_up_sync(0xffffffffu, v.rows, o);
+    if (lane >= o) {
+      v.pages += a;
+      v.rows += b;
+    }
   }
+  return v;
+}
+__device__ __forceinline__ Two block_scan(Two v, Two* s_warp, Two& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  v = warp_scan(v, lane);
   __syncthreads();                          // s_warp may still be read from the last scan
   if (lane == 31) s_warp[warp] = v;
   __syncthreads();
-  unsigned long long before = 0, all = 0;
-  for (int w = 0; w < nw; ++w) {
-    const unsigned long long u = s_warp[w];
-    if (w < warp) before += u;
-    all += u;
-  }
-  total = all;
-  return v + before;
+  // every warp scans the warps' sums
+  const Two w = warp_scan(lane < nw ? s_warp[lane] : Two{0, 0}, lane);
+  const int from = (warp + 31) & 31;
+  const Two before{__shfl_sync(0xffffffffu, w.pages, from), __shfl_sync(0xffffffffu, w.rows, from)};
+  total = Two{__shfl_sync(0xffffffffu, w.pages, 31), __shfl_sync(0xffffffffu, w.rows, 31)};
+  return warp ? Two{v.pages + before.pages, v.rows + before.rows} : v;
 }
 
 // Last b in [0, n) with ptr[b] <= x (ptr ascending, ptr[0] <= x).
@@ -103,7 +111,7 @@ __device__ __forceinline__ int last_at_or_below(const int* ptr, int n, int x) {
 
 __global__ void __launch_bounds__(1024) block_tables_kernel(TablesParams p) {
   extern __shared__ int s_tab[];            // [5][B + 1]
-  __shared__ unsigned long long s_warp[32];
+  __shared__ Two s_warp[32];
   __shared__ int s_first;
   const int B = p.B, n1 = B + 1;
   int* s_row = s_tab;                       // first row of each request
@@ -149,8 +157,12 @@ __global__ void __launch_bounds__(1024) block_tables_kernel(TablesParams p) {
       pages += d > 0 ? (unsigned long long)d : (unsigned long long)(-d) << 32;
       rows += (unsigned long long)r[i].add;
     }
-    pages_at = block_scan(pages, s_warp, total_pages) - pages;
-    rows_at = block_scan(rows, s_warp, total_rows) - rows;
+    Two all;
+    const Two upto = block_scan(Two{pages, rows}, s_warp, all);
+    total_pages = all.pages;
+    total_rows = all.rows;
+    pages_at = upto.pages - pages;
+    rows_at = upto.rows - rows;
     const bool fits = (long long)(total_pages & 0xffffffffu) <= free_pages &&
                       total_rows <= (unsigned long long)p.max_rows;
     if (fits || pass) break;                // uniform over the CTA
@@ -173,7 +185,7 @@ __global__ void __launch_bounds__(1024) block_tables_kernel(TablesParams p) {
     for (int i = 0; i < TABLES_ITEMS; ++i)
       if (i < items && b0 + i < B && b0 + i >= first && r[i].add > 0) {
         r[i].add = 0;
-        r[i].need = (r[i].base + p.P - 1) / p.P;
+        r[i].need = (int)(((long long)r[i].base + p.P - 1) >> p.page_bits);
         flags |= SPEC_DEV_NO_PAGES;
       }
   }
@@ -210,12 +222,17 @@ __global__ void __launch_bounds__(1024) block_tables_kernel(TablesParams p) {
   __syncthreads();
 
   const int gid = blockIdx.x * blockDim.x + threadIdx.x, gsz = gridDim.x * blockDim.x;
+  // entry of the m-th page taken: m < n_ask <= free pages <= num_pages, so one
+  // subtraction is the remainder
+  auto taken = [&](int m) {
+    const uint32_t at = (uint32_t)head_at + (uint32_t)m;
+    return at >= (uint32_t)p.num_pages ? at - (uint32_t)p.num_pages : at;
+  };
   // pages that change hands
   for (int m = gid; m < n_ask + n_give; m += gsz) {
     if (m < n_ask) {
       const int b = last_at_or_below(s_ask, B, m);
-      const uint32_t at = ((uint32_t)head_at + m) % p.num_pages;
-      p.table[(size_t)b * p.stride + s_held[b] + (m - s_ask[b])] = p.ring[at];
+      p.table[(size_t)b * p.stride + s_held[b] + (m - s_ask[b])] = p.ring[taken(m)];
     } else {
       const int g = m - n_ask, b = last_at_or_below(s_give, B, g);
       const int count = (b + 1 < B ? s_give[b + 1] : n_give) - s_give[b];
@@ -227,6 +244,7 @@ __global__ void __launch_bounds__(1024) block_tables_kernel(TablesParams p) {
   for (long long r4 = (long long)gid * 4; r4 < p.max_rows; r4 += (long long)gsz * 4) {
     int slot[4], pos[4];
     int b = r4 < n_rows ? last_at_or_below(s_row, B, (int)r4) : 0;
+    int last_b = -1, last_blk = 0, page = 0;                 // the page of the row before
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = (int)r4 + i;
@@ -234,15 +252,15 @@ __global__ void __launch_bounds__(1024) block_tables_kernel(TablesParams p) {
       if (row >= n_rows) continue;
       while (s_row[b + 1] <= row) ++b;
       pos[i] = s_base[b] + row - s_row[b];
-      const int blk = pos[i] / p.P, held = s_held[b];
-      int page;
-      if (blk < held) {
-        page = __ldg(p.table + (size_t)b * p.stride + blk);
-      } else {
-        page = p.ring[((uint32_t)head_at + s_ask[b] + blk - held) % p.num_pages];
+      const int blk = pos[i] >> p.page_bits;
+      if (b != last_b || blk != last_blk) {
+        const int held = s_held[b];
+        page = blk < held ? __ldg(p.table + (size_t)b * p.stride + blk) : p.ring[taken(s_ask[b] + blk - held)];
+        last_b = b;
+        last_blk = blk;
       }
       if (page < 0 || page >= p.num_pages) flags |= SPEC_DEV_BAD_SLOT;
-      else slot[i] = page * p.P + pos[i] - blk * p.P;
+      else slot[i] = (page << p.page_bits) + (pos[i] & (p.P - 1));
     }
     if (r4 + 4 <= p.max_rows) {
       *reinterpret_cast<int4*>(p.slots + r4) = make_int4(slot[0], slot[1], slot[2], slot[3]);
@@ -260,7 +278,7 @@ __global__ void __launch_bounds__(1024) block_tables_kernel(TablesParams p) {
 }
 
 cudaError_t launch_block_tables(const spec_block_tables_args& a, int sms, cudaStream_t st) {
-  TablesParams p{a.B, a.page_size, a.num_pages, a.table_stride, a.max_rows, a.seq_len, a.accept_len, a.new_len,
+  TablesParams p{a.B, a.page_size, __builtin_ctz(a.page_size), a.num_pages, a.table_stride, a.max_rows, a.seq_len, a.accept_len, a.new_len,
                  a.num_blocks, (const long long*)a.ring_pos, a.free_ring, a.block_table, a.seq_len_out, a.kv_len,
                  a.num_blocks_out, (long long*)a.ring_pos_out, a.row_ptr, a.slots, a.positions, a.dev_status};
   const int threads = a.B <= 256 ? 256 : 1024;
