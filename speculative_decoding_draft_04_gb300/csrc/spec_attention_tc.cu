@@ -243,8 +243,7 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
   auto wait2 = [&](int pair, uint32_t x) { wait(bar + pair + (x & 1), (x >> 1) & 1); };
   auto arrive = [&](uint64_t* b) {
     __syncwarp();
-    if (lane == 0)
-      asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(b)) : "memory");
+    if (lane == 0) mbar_arrive1(b);
   };
   AttnSplit split{0, -1, 0, 0, 0, 0, 0};
 

@@ -116,3 +116,22 @@ def test_strides_streams_and_repeats(torch):
         assert (np.abs(l[:p.T] - lse) <= tol_l).all()
         assert first is None or (out == first).all()       # bit for bit
         first = out
+
+
+def test_offsets_beyond_2_to_the_32(torch):
+    rng = np.random.default_rng(11)
+    p = H.Paged(rng, [90, 200], [36, 50], 4, 2, 128, 64, "bf16")
+    small = p.cache
+    per = int(np.prod(small.shape[1:]))
+    far = (9 << 30) // per
+    big = torch.zeros((far + len(small), *small.shape[1:]), dtype=torch.uint8, device="cuda")
+    big[far:] = H.dev(small)
+    L = H.lib()
+    q, st = H.dev(p.q, torch.bfloat16), H.new_status()
+    out = torch.empty_like(q)
+    ws = torch.empty(L.spec_cache_attention_workspace_bytes(4, 2, 128), dtype=torch.uint8, device="cuda")
+    table = H.dev(np.where(p.table >= 0, p.table + far, -1).astype(np.int32))
+    L.spec_cache_attention(q, big, table, H.dev(p.lens), H.dev(p.ptr), out, st, ws, 0.1, p.k_scale, p.v_scale)
+    torch.cuda.synchronize()
+    want, _, tol, _ = p.oracle(0.1)
+    assert H.status(st) == 0 and (np.abs(out.double().cpu().numpy() - want) <= tol).all()
