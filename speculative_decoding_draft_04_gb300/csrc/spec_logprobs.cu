@@ -180,16 +180,19 @@ __global__ void __launch_bounds__(LP_THREADS, 2) logprobs_kernel(const __grid_co
 #pragma unroll
     for (int j = 0; j < LP_VECS; ++j) vm[j] = vec_max(v[j], tag);
   } else {
-    int edge = -1;                                           // this thread's vector that the row fills in part
+    uint32_t edges = 0;                                      // this thread's vectors that the row fills in part:
+                                                             // its first and its last may be one thread's
 #pragma unroll
     for (int j = 0; j < LP_VECS; ++j) {
       const int at = (i0 + j * LP_THREADS) * E - lead;
       const uint32_t w = low_word(tag);
       v[j] = make_uint4(w, w, w, w);
       if (at >= 0 && at + E <= p.V) v[j] = __ldcs(reinterpret_cast<const uint4*>(x + at));
-      else if (at + E > 0 && at < p.V) edge = j;
+      else if (at + E > 0 && at < p.V) edges |= 1u << j;
     }
-    if (edge >= 0) {
+    while (edges) {
+      const int edge = __ffs(edges) - 1;
+      edges &= edges - 1;
       const uint4 q = edge_vector(x, (i0 + edge * LP_THREADS) * E - lead, p.V);
 #pragma unroll
       for (int j = 0; j < LP_VECS; ++j)
