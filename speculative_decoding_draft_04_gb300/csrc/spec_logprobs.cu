@@ -222,6 +222,9 @@ __global__ void __launch_bounds__(LP_THREADS, 2) logprobs_kernel(const __grid_co
   // ---- sums against the warp's maximum; an entry of -inf adds nothing
   const float c = 1.4426950408889634f / T;
   const float base = m == -INFINITY ? 0.f : -m * c;
+  // the distance that the maximum gets: the rounding of m c, exactly.  Every
+  // distance of the warp holds it, so Z and sum 2^d d are cleared of it below.
+  float off = m == -INFINITY ? 0.f : fmaf(m, c, base);
   float z = 0.f, w1 = 0.f;
   {
     const uint64_t c2 = pair(c, c), b2 = pair(base, base);
@@ -240,10 +243,11 @@ __global__ void __launch_bounds__(LP_THREADS, 2) logprobs_kernel(const __grid_co
     z = zs.x + zs.y;
     w1 = ws.x + ws.y;
   }
-  if (__any_sync(0xffffffffu, !(fabsf(w1) <= 3.4e38f))) {
-    // an entry of -inf (0 times its distance), or numbers near the floats' end:
+  if (__any_sync(0xffffffffu, !(fabsf(w1) <= 3.4e38f)) || !(fabsf(off) <= 1.f)) {
+    // an entry of -inf (0 times its distance), numbers near the floats' end, or
+    // |m c| beyond 2^24, where `off` would cost the distances their last bits:
     // once more, distances first and bounded
-    z = w1 = 0.f;
+    z = w1 = off = 0.f;
     for (int j = 0; j < LP_VECS; ++j) {
       const int at = (i0 + j * LP_THREADS) * E - lead;
       float zz = 0.f, ww = 0.f;
@@ -263,7 +267,13 @@ __global__ void __launch_bounds__(LP_THREADS, 2) logprobs_kernel(const __grid_co
     z += __shfl_xor_sync(0xffffffffu, z, o);
     w1 += __shfl_xor_sync(0xffffffffu, w1, o);
   }
-  if (lane == 0) s_warp[warp] = make_float4(m, m == -INFINITY ? 0.f : z, m == -INFINITY ? 0.f : w1, 0.f);
+  if (lane == 0) {
+    // the maximum itself counts 1, whatever 2^off 2^-off is rounded to
+    const float f = ex2(-off);
+    w1 = f * fmaf(-off, z, w1);
+    z = fmaxf(z * f, 1.f);
+    s_warp[warp] = make_float4(m, m == -INFINITY ? 0.f : z, m == -INFINITY ? 0.f : w1, 0.f);
+  }
   __syncthreads();
   // ---- bound of the candidates: the K-th largest group maximum
   if (p.K > 0) {
