@@ -92,9 +92,12 @@ __device__ __forceinline__ float vec_get(const uint4& v, int e, const float*) {
 }
 __device__ __forceinline__ uint32_t neg_inf_word(const bf16*) { return 0xff80ff80u; }
 __device__ __forceinline__ uint32_t neg_inf_word(const float*) { return 0xff800000u; }
-// A value below every entry that counts, finite so that 0 times its distance is 0.
-__device__ __forceinline__ uint32_t low_word(const bf16*) { return 0xf14af14au; }     // -1e30
+// What fills vectors without an entry: about -1e30, far below the entries of most
+// rows, and finite so that 0 times its distance is 0.
+__device__ __forceinline__ uint32_t low_word(const bf16*) { return 0xf14af14au; }
 __device__ __forceinline__ uint32_t low_word(const float*) { return 0xf149f2cau; }
+__device__ __forceinline__ float low_value(const bf16*) { return __uint_as_float(0xf14a0000u); }
+__device__ __forceinline__ float low_value(const float*) { return __uint_as_float(0xf149f2cau); }
 // Bits of an element.
 __device__ __forceinline__ uint32_t bits_of(bf16 x) { return *reinterpret_cast<const uint16_t*>(&x); }
 __device__ __forceinline__ uint32_t bits_of(float x) { return __float_as_uint(x); }
@@ -173,7 +176,8 @@ __global__ void __launch_bounds__(LP_THREADS, 2) logprobs_kernel(const __grid_co
   const int i0 = seg * (SEG / E) + tid;
   uint4 v[LP_VECS];
   float vm[LP_VECS], tm;
-  if (seg * SEG >= lead && (seg + 1) * SEG - lead <= p.V) {  // uniform: a segment that the row fills
+  const bool full = seg * SEG >= lead && (seg + 1) * SEG - lead <= p.V;   // uniform: a segment that the row fills
+  if (full) {
     const uint4* at = reinterpret_cast<const uint4*>(x + (i0 * E - lead));
 #pragma unroll
     for (int j = 0; j < LP_VECS; ++j) v[j] = __ldcs(at + j * LP_THREADS);
@@ -243,10 +247,13 @@ __global__ void __launch_bounds__(LP_THREADS, 2) logprobs_kernel(const __grid_co
     z = zs.x + zs.y;
     w1 = ws.x + ws.y;
   }
-  if (__any_sync(0xffffffffu, !(fabsf(w1) <= 3.4e38f)) || !(fabsf(off) <= 1.f)) {
-    // an entry of -inf (0 times its distance), numbers near the floats' end, or
-    // |m c| beyond 2^24, where `off` would cost the distances their last bits:
-    // once more, distances first and bounded
+  // a filler whose exponential is not 0: entries as low as it, or a temperature
+  // beside which it is near them
+  const bool filler = !full && fmaf(low_value(tag), c, base) > -127.f;
+  if (__any_sync(0xffffffffu, !(fabsf(w1) <= 3.4e38f)) || !(fabsf(off) <= 1.f) || filler) {
+    // an entry of -inf (0 times its distance), numbers near the floats' end, |m c|
+    // beyond 2^24, where `off` would cost the distances their last bits, or a
+    // filler that counts: once more, distances first and bounded
     z = w1 = off = 0.f;
     for (int j = 0; j < LP_VECS; ++j) {
       const int at = (i0 + j * LP_THREADS) * E - lead;
