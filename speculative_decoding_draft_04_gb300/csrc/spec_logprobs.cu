@@ -125,6 +125,18 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// Distances below a maximum as multiples of T / log2(e), not under -200 (where 2^d
+// is 0): differences times `up`, then times c.  up = 1 but for a T below the normal
+// numbers, whose own quotient would be infinite.
+struct Distance {
+  float up, c;
+  __device__ __forceinline__ explicit Distance(float T) {
+    up = T < 1.17549435e-38f ? 0x1p24f : 1.f;
+    c = 1.4426950408889634f / (T * up);
+  }
+  __device__ __forceinline__ float operator()(float below) const { return fmaxf(below * up * c, -200.f); }
+};
+
 // What of a row can be said before its entries are read: bits of dev_status, or
 // ~0 for a padding row.
 __device__ __forceinline__ uint32_t row_flag(const LogprobParams& p, int token, float T) {
@@ -224,7 +236,8 @@ __global__ void __launch_bounds__(LP_THREADS, 2) logprobs_kernel(const __grid_co
 #pragma unroll
   for (int o = 4; o < 32; o <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   // ---- sums against the warp's maximum; an entry of -inf adds nothing
-  const float c = 1.4426950408889634f / T;
+  const Distance distance(T);
+  const float c = distance.c;
   const float base = m == -INFINITY ? 0.f : -m * c;
   // the distance that the maximum gets: the rounding of m c, exactly.  Every
   // distance of the warp holds it, so Z and sum 2^d d are cleared of it below.
@@ -250,17 +263,17 @@ __global__ void __launch_bounds__(LP_THREADS, 2) logprobs_kernel(const __grid_co
   // a filler whose exponential is not 0: entries as low as it, or a temperature
   // beside which it is near them
   const bool filler = !full && fmaf(low_value(tag), c, base) > -127.f;
-  if (__any_sync(0xffffffffu, !(fabsf(w1) <= 3.4e38f)) || !(fabsf(off) <= 1.f) || filler) {
+  if (__any_sync(0xffffffffu, !(fabsf(w1) <= 3.4e38f)) || !(fabsf(off) <= 1.f) || filler || distance.up != 1.f) {
     // an entry of -inf (0 times its distance), numbers near the floats' end, |m c|
-    // beyond 2^24, where `off` would cost the distances their last bits, or a
-    // filler that counts: once more, distances first and bounded
+    // beyond 2^24, where `off` would cost the distances their last bits, a filler
+    // that counts, or a subnormal T: once more, distances first and bounded
     z = w1 = off = 0.f;
     for (int j = 0; j < LP_VECS; ++j) {
       const int at = (i0 + j * LP_THREADS) * E - lead;
       float zz = 0.f, ww = 0.f;
       for (int e = max(0, -at); e < E && at + e < p.V; ++e) {
         const float y = tof(x[at + e]);
-        const float d = y == -INFINITY ? -200.f : fmaxf((y - m) * c, -200.f);
+        const float d = y == -INFINITY ? -200.f : distance(y - m);
         const float q = ex2(d);
         zz += q;
         ww = fmaf(q, d, ww);
@@ -332,7 +345,7 @@ __global__ void __launch_bounds__(LP_THREADS, 2) logprobs_kernel(const __grid_co
 #pragma unroll
   for (int i = 0; i < LP_WARPS; ++i) {
     const float4 q = s_warp[i];
-    const float d = q.x == -INFINITY ? 0.f : fmaxf((q.x - pm) * c, -200.f), f = ex2(d);
+    const float d = q.x == -INFINITY ? 0.f : distance(q.x - pm), f = ex2(d);
     pz += q.y * f;
     pw += f * fmaf(q.y, d, q.z);
   }
@@ -422,11 +435,11 @@ __global__ void __launch_bounds__(32 * LPJ_WARPS) logprobs_join_kernel(const __g
       write_nothing(p, row, lane, 32, SPEC_DEV_BAD_LOGIT);
       return;
     }
-    const float c = 1.4426950408889634f / T;
+    const Distance distance(T);
     float z = 0.f, w1 = 0.f;
     for (int s = lane; s < p.segments; s += 32) {
       const float4 q = part[s];
-      const float d = q.x == -INFINITY ? 0.f : fmaxf((q.x - m) * c, -200.f), f = ex2(d);
+      const float d = q.x == -INFINITY ? 0.f : distance(q.x - m), f = ex2(d);
       z += q.y * f;
       w1 += f * fmaf(q.y, d, q.z);
     }
