@@ -8,7 +8,7 @@
 // One thread a group; a warp covers consecutive tokens of one head, so codes and
 // scales of neighbouring slots leave in whole sectors.  The quotients are those
 // of IEEE division, from the rounded reciprocal y of r = s g: q = x y,
-// q + (x - q r) y with fused multiply-adds is the rounded quotient (P. Markstein,
+// q - (q r - x) y with fused multiply-adds is the rounded quotient (P. Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000 processor",
 // IBM J. Res. Dev. 34, 1990).  That holds while nothing over- or underflows:
 // |x| <= 8 r here, and where x - q r is below the normal numbers, x / r is below
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) cache_append_kernel(const __gr
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const float q = __fmul_rn(x[e], y);
-        x[e] = __fmaf_rn(__fmaf_rn(-q, r, x[e]), y, q);
+        x[e] = __fmaf_rn(-__fmaf_rn(q, r, -x[e]), y, q);   // this way round, -0 / r stays -0
       }
       w[0] = encode8(x);
       w[1] = encode8(x + 8);
