@@ -37,7 +37,7 @@ class Target:
         T, Hq, Hkv, D = x.shape[0], self.Hq, self.Hkv, self.D
         for i, (wi, wo) in enumerate(zip(self.qkv, self.proj)):
             y = (torch.nn.functional.rms_norm(x, x.shape[1:]) @ wi).view(T, Hq + 2 * Hkv, D)
-            o = torch.empty((T, Hq, D), dtype=x.dtype, device=x.device)
+            o = torch.zeros((T, Hq, D), dtype=x.dtype, device=x.device)
             engine.attend(c, i, y[:, :Hq], y[:, Hq:Hq + Hkv], y[:, Hq + Hkv:], o)
             x = x + o.view(T, Hq * D) @ wo
         x = x if last is None else x[last]
@@ -45,9 +45,11 @@ class Target:
 
 
 def serve(requests=8, cycles=4, prompt=100, gamma=7, V=32000, width=512, layers=2, Hq=16, Hkv=4, D=64,
-          page_size=32, top=5, seed=0):
+          page_size=32, top=5, seed=0, pages=None):
     """Per cycle: tokens emitted (int32 [B, gamma + 1], -1 padded), their log
-    probabilities, and the cache with the lengths of its requests."""
+    probabilities, and the cache with the lengths of its requests.  pages: of
+    the pool, by default enough for every request; a request that finds none
+    for its block emits nothing in that cycle and goes on when there are."""
     gen = torch.Generator("cuda").manual_seed(seed)
     B, n = requests, gamma + 1
     model = Target(V, width, layers, Hq, Hkv, D, gen)
@@ -58,7 +60,7 @@ def serve(requests=8, cycles=4, prompt=100, gamma=7, V=32000, width=512, layers=
     l = engine.DeviceLogprobs.allocate(B, n, V, K=top)
     most = prompt + B + (cycles + 1) * n                      # tokens of the longest request
     rows = B * prompt + B * (B - 1) // 2
-    c = engine.DeviceCache.allocate(B, layers, Hq, Hkv, D, page_size, B * -(-most // page_size), most,
+    c = engine.DeviceCache.allocate(B, layers, Hq, Hkv, D, page_size, pages or B * -(-most // page_size), most,
                                     max(rows, B * n), [0.01] * layers, [0.01] * layers)
     # prompts, one token longer from request to request; the last token of each
     # becomes the first anchor
@@ -69,9 +71,18 @@ def serve(requests=8, cycles=4, prompt=100, gamma=7, V=32000, width=512, layers=
     d.anchor.copy_(first.argmax(-1))
     block = torch.full((B,), n, dtype=torch.int32, device="cuda")
 
+    row = torch.arange(B * n, device="cuda")
+
     def target_pass(d, b, c, stream):
-        fed = torch.cat([d.anchor[:, None], b.draft_tokens], 1).reshape(-1)
-        d.target.copy_(model(fed, c).view(B, n, V))
+        # packed row r is token r - row_ptr[i] of the i-th request's block; a
+        # request without pages for its block has no rows (those beyond
+        # row_ptr[B] belong to nobody)
+        ptr = c.row_ptr.long()
+        who = torch.searchsorted(ptr[1:], row, right=True).clamp(max=B - 1)
+        fed = torch.cat([d.anchor[:, None], b.draft_tokens], 1)
+        logits = model(fed[who, (row - ptr[who]).clamp(max=n - 1)], c)
+        at = (ptr[:-1, None] + row[:n]).clamp(max=B * n - 1)
+        d.target.copy_(logits[at])
 
     kept, out = held - 1, []
     for _ in range(cycles):
@@ -79,9 +90,11 @@ def serve(requests=8, cycles=4, prompt=100, gamma=7, V=32000, width=512, layers=
             u.uniform_(generator=gen)
         engine.served_cycle(d, b, c, l, target_pass, block, kept)
         kept = b.accept_len.clone()
-        d.anchor.copy_(b.out_tokens.gather(1, kept[:, None].long())[:, 0])
+        newest = b.out_tokens.gather(1, kept.clamp(min=0)[:, None].long())[:, 0]
+        d.anchor.copy_(torch.where(kept < 0, d.anchor, newest))
         out.append((b.out_tokens.clone(), l.logprob.clone()))
     words = [engine.status_words(t)[0] for t in (b.dstatus, b.vstatus, c.status, l.status)]
+    words[2] &= ~256                                          # pages that were not there
     if any(words):
         raise RuntimeError(f"status words {words}")
     return out, c

@@ -454,8 +454,9 @@ size_t spec_cache_bytes(int32_t num_pages, int32_t Hkv, int32_t page_size, int32
 
 /* spec_block_tables: block tables and slot maps from request lengths, in one
  * launch.  Request b keeps base = seq_len + accept_len + 1 tokens (accept_len
- * as spec_verify wrote it; -1 keeps nothing new; a NULL accept_len array
- * keeps seq_len) and appends new_len tokens; new_len = -1 is a finished
+ * as spec_verify wrote it; -1 keeps nothing new, and is what a request that
+ * had no rows in the last block must be given; a NULL accept_len array keeps
+ * seq_len) and appends new_len tokens; new_len = -1 is a finished
  * request, which keeps nothing.  kv_len = base + new_len tokens need
  * ceil(kv_len / page_size) pages: missing ones are taken from the ring of
  * free pages in request order, surplus ones go back to it in request order.

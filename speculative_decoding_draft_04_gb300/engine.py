@@ -380,8 +380,9 @@ class DeviceCache:
 def make_room(c: DeviceCache, new_len, accept_len=None, stream=None) -> None:
     """Keep what the last block's verification accepted and make room for each
     request's new_len next tokens.  accept_len counts the kept tokens of the
-    last block beyond its first (prompt length - 1 after a prompt); None keeps
-    nothing of it, as before the first block."""
+    last block beyond its first (prompt length - 1 after a prompt), -1 where
+    the request had no rows in it (see drop_absent); None keeps nothing of it,
+    as before the first block."""
     old, new = c.newest, 1 - c.newest
     _lib.spec_block_tables(c.seq_len[old], accept_len, new_len, c.num_blocks[old], c.ring_pos[old],
                            c.free_ring, c.block_table, c.seq_len[new], c.kv_len, c.num_blocks[new],
@@ -432,6 +433,19 @@ def logprobs(logits, tokens, temperature, l: DeviceLogprobs, stream=None) -> Non
                        stream=stream)
 
 
+def drop_absent(c: DeviceCache, accept_len, out_tokens, stream=None) -> None:
+    """What verification says of requests without rows in the newest step
+    (refused for want of pages, finished, or of no new tokens) was not said of
+    any token of theirs: accept_len and out_tokens become -1."""
+    import contextlib
+
+    import torch
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        absent = c.row_ptr[1:] == c.row_ptr[:-1]
+        accept_len.masked_fill_(absent, -1)
+        out_tokens.masked_fill_(absent[:, None], -1)
+
+
 def served_cycle(d: DeviceWorkload, b: Buffers, c: DeviceCache, l: DeviceLogprobs, target_pass,
                  new_len, accept_len=None, stream=None) -> None:
     """One cycle of a server: draft, keep what the last cycle accepted and make
@@ -439,12 +453,15 @@ def served_cycle(d: DeviceWorkload, b: Buffers, c: DeviceCache, l: DeviceLogprob
     probabilities of the emitted tokens.  target_pass(d, b, c, stream) enqueues
     the model's layers, each with ``attend``, and leaves its logits in
     d.target; new_len is gamma + 1 per request (the anchor and the block), 1 +
-    verify_len where lengths are scheduled.  b.accept_len of this cycle is
-    accept_len of the next."""
+    verify_len where lengths are scheduled.  A request that gets no rows (no
+    pages for them, new_len -1 or 0) emits nothing: its accept_len and
+    out_tokens are -1, whatever d.target holds for it.  So b.accept_len of this
+    cycle is accept_len of the next for every request."""
     draft(d, b, stream)
     make_room(c, new_len, accept_len, stream)
     target_pass(d, b, c, stream)
     verify(d, b, stream)
+    drop_absent(c, b.accept_len, b.out_tokens, stream)
     logprobs(d.target, b.out_tokens, d.temperature, l, stream)
 
 
