@@ -190,12 +190,15 @@ __global__ void __launch_bounds__(1024) block_tables_kernel(TablesParams p) {
       }
   }
 
+  // a ring that cannot be takes no pages back: requests keep them
+  const bool keep = bad_ring;
   {
-    int ask = (int)(pages_at & 0xffffffffu), give = (int)(pages_at >> 32), row = (int)rows_at;
+    int ask = (int)(pages_at & 0xffffffffu), give = keep ? 0 : (int)(pages_at >> 32), row = (int)rows_at;
 #pragma unroll
     for (int i = 0; i < TABLES_ITEMS; ++i) {
       const int b = b0 + i;
       if (i >= items || b >= B) break;
+      if (keep && r[i].need < r[i].held) r[i].need = r[i].held;
       s_row[b] = row;
       s_ask[b] = ask;
       s_give[b] = give;
@@ -212,7 +215,7 @@ __global__ void __launch_bounds__(1024) block_tables_kernel(TablesParams p) {
       row += r[i].add;
     }
   }
-  const int n_rows = (int)total_rows, n_ask = (int)(total_pages & 0xffffffffu), n_give = (int)(total_pages >> 32);
+  const int n_rows = (int)total_rows, n_ask = (int)(total_pages & 0xffffffffu), n_give = keep ? 0 : (int)(total_pages >> 32);
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     p.row_ptr[B] = n_rows;
     p.ring_pos_out[0] = head + n_ask;
