@@ -470,7 +470,9 @@ size_t spec_cache_bytes(int32_t num_pages, int32_t Hkv, int32_t page_size, int32
  * rows; a page id outside [0, num_pages) sets SPEC_DEV_BAD_SLOT and the
  * row's slot is -1.  A ring whose head is negative or whose tail - head is not
  * in [0, num_pages] sets SPEC_DEV_BAD_LEN: no page is taken, none is given
- * back (requests keep them), and ring_pos_out is ring_pos.
+ * back (requests keep them), and ring_pos_out is ring_pos.  If free and given
+ * pages are more than num_pages together, none is given back either, with the
+ * same bit.
  * Row i of the packed rows (request order, row_ptr) is token positions[i] of
  * its request at slot slots[i]; rows from row_ptr[B] to max_rows get -1.
  * Table entries at and beyond num_blocks_out are left as they are, so a call

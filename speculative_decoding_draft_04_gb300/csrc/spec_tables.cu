@@ -190,8 +190,12 @@ __global__ void __launch_bounds__(1024) block_tables_kernel(TablesParams p) {
       }
   }
 
-  // a ring that cannot be takes no pages back: requests keep them
-  const bool keep = bad_ring;
+  // a ring that cannot be, or that has no room for what comes back (a page that
+  // is free and held at once: entries to write would be entries that other
+  // threads read), takes nothing: requests keep their pages
+  const bool over = free_pages + (long long)(total_pages >> 32) > p.num_pages;
+  if (over) flags |= SPEC_DEV_BAD_LEN;
+  const bool keep = bad_ring || over;
   {
     int ask = (int)(pages_at & 0xffffffffu), give = keep ? 0 : (int)(pages_at >> 32), row = (int)rows_at;
 #pragma unroll
