@@ -8,9 +8,11 @@
 //       contiguous, any dtype; address, row stride, head stride of [T][H][D].
 //       t None: 0 where `what` ends in '?', else refused.
 #include <c10/core/ScalarType.h>
+#include <c10/util/Exception.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <exception>
 #include <string>
 
 namespace {
@@ -53,7 +55,7 @@ PyObject* use(PyObject*, PyObject* error) {
   Py_RETURN_NONE;
 }
 
-PyObject* addresses(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* checked_addresses(PyObject* const* a, Py_ssize_t n) {
   constexpr Py_ssize_t MOST = 64;
   long long out[MOST];
   Py_ssize_t m = 0;
@@ -88,8 +90,28 @@ PyObject* addresses(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   PyObject* r = PyTuple_New(m);
   if (!r) return nullptr;
-  for (Py_ssize_t i = 0; i < m; ++i) PyTuple_SET_ITEM(r, i, PyLong_FromLongLong(out[i]));
+  for (Py_ssize_t i = 0; i < m; ++i) {
+    PyObject* v = PyLong_FromLongLong(out[i]);
+    if (!v) {
+      Py_DECREF(r);
+      return nullptr;
+    }
+    PyTuple_SET_ITEM(r, i, v);
+  }
   return r;
+}
+
+// torch throws where a kind of tensor has no sizes, strides or address.
+PyObject* addresses(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  try {
+    return checked_addresses(a, n);
+  } catch (const c10::Error& e) {
+    return refuse(std::string("not a plain tensor: ") + e.what_without_backtrace());
+  } catch (const std::exception& e) {
+    return refuse(e.what());
+  } catch (...) {
+    return refuse("an unknown exception in the checks of tensors");
+  }
 }
 
 PyMethodDef methods[] = {
