@@ -481,6 +481,10 @@ def _types():
         except ImportError as e:
             raise SpecError(f"the compiled checks are missing ({e}): build them with "
                             "speculative_decoding_draft_04_gb300.build.build()") from e
+        from .build import built_for
+        if checks.built_for != built_for():              # before it reads any of this torch's objects
+            raise SpecError(f"the compiled checks were built for {checks.built_for}, this is {built_for()}: build "
+                            "them again with speculative_decoding_draft_04_gb300.build.build()")
         checks.use(SpecError)
         _torch, _args = torch, checks
     return _torch

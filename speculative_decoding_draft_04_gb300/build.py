@@ -3,8 +3,10 @@
 Each CUDA translation unit is compiled in parallel with nvcc and linked into
 ``libspec.so`` next to this file.  The CUDA runtime is linked statically, so
 the library only needs the driver at run time.  Beside it, the binding's checks
-of tensor arguments are compiled into the Python module ``_args``.  Rebuilds only
-when a source or header is newer than either.
+of tensor arguments are compiled into the Python module ``_args``, which reads
+torch's C++ objects: it is named for its Python and records the torch that it
+was built with.  Rebuilds what a source or header is newer than, and ``_args``
+for another torch.
 """
 from __future__ import annotations
 
@@ -19,7 +21,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libspec.so")
-ARGS = os.path.join(HERE, "_args.so")
+ARGS = os.path.join(HERE, "_args" + sysconfig.get_config_var("EXT_SUFFIX"))
+ARGS_FOR = os.path.join(OBJDIR, "args_for.txt")     # what ARGS was built for
 SOURCES = ["spec_abi.cu", "spec_draft.cu", "spec_draft_slice.cu", "spec_verify.cu",
            "spec_verify_slice.cu", "spec_verify_redecide.cu", "spec_refine.cu", "spec_report.cu",
            "spec_sched.cu", "spec_tree.cu", "spec_tables.cu", "spec_cache.cu", "spec_attention.cu", "spec_attention_tc.cu",
@@ -36,17 +39,33 @@ def _nvcc() -> str:
     return cand
 
 
-def _inputs() -> list[str]:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".cpp"))]
-    files.append(os.path.join(INCLUDE, "spec.h"))
-    return files
+def _newer(than: str, *suffixes: str) -> bool:
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(suffixes)]
+    if ".cu" in suffixes:
+        files.append(os.path.join(INCLUDE, "spec.h"))
+    t = os.path.getmtime(than)
+    return any(os.path.getmtime(f) > t for f in files)
+
+
+def built_for() -> str:
+    """The torch whose objects ``_args`` reads."""
+    import torch
+    return f"torch {torch.__version__} {torch.version.git_version}"
+
+
+def _lib_stale() -> bool:
+    return not os.path.exists(LIB) or _newer(LIB, ".cu", ".cuh")
+
+
+def _args_stale() -> bool:
+    if not (os.path.exists(ARGS) and os.path.exists(ARGS_FOR)) or _newer(ARGS, ".cpp"):
+        return True
+    with open(ARGS_FOR) as f:
+        return f.read() != built_for()
 
 
 def is_stale() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(ARGS)):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(ARGS))
-    return any(os.path.getmtime(f) > t for f in _inputs())
+    return _lib_stale() or _args_stale()
 
 
 def _build_args() -> None:
@@ -56,6 +75,7 @@ def _build_args() -> None:
     tmp = ARGS + ".tmp"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f'-DSPEC_BUILT_FOR="{built_for()}"',
            "-I" + sysconfig.get_paths()["include"], "-I" + inc,
            "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
            os.path.join(CSRC, "spec_args.cpp"), "-o", tmp, "-L" + os.path.join(home, "lib"),
@@ -64,14 +84,19 @@ def _build_args() -> None:
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed on spec_args.cpp:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, ARGS)
+    with open(ARGS_FOR, "w") as f:
+        f.write(built_for())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libspec.so and _args.so; returns the library's path."""
-    if not force and not is_stale():
+    """Compile and link libspec.so and _args; returns the library's path."""
+    os.makedirs(OBJDIR, exist_ok=True)
+    args_stale = force or _args_stale()
+    if not force and not _lib_stale():
+        if args_stale:
+            _build_args()
         return LIB
     nvcc = _nvcc()
-    os.makedirs(OBJDIR, exist_ok=True)
 
     def compile_one(src: str) -> str:
         obj = os.path.join(OBJDIR, src.replace(".cu", ".o"))
@@ -84,9 +109,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        args = ex.submit(_build_args)
+        args = ex.submit(_build_args) if args_stale else None
         objs = list(ex.map(compile_one, SOURCES))
-        args.result()
+        if args:
+            args.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)
