@@ -468,12 +468,13 @@ def _format(py) -> struct.Struct:
 _TABLES, _APPEND = _format(BlockTablesArgs), _format(CacheAppendArgs)
 _ATTENTION, _LOGPROBS = _format(CacheAttentionArgs), _format(LogprobsArgs)
 _torch = _args = None
+_device = None              # the current device: launches go to it, so every tensor and the stream have to be on it
 
 
 def _types():
     """torch, imported at the first call that needs it, with the module that
     checks tensors."""
-    global _torch, _args
+    global _torch, _args, _device
     if _torch is None:
         import torch
         try:
@@ -486,14 +487,17 @@ def _types():
             raise SpecError(f"the compiled checks were built for {checks.built_for}, this is {built_for()}: build "
                             "them again with speculative_decoding_draft_04_gb300.build.build()")
         checks.use(SpecError)
+        _device = torch._C._cuda_getDevice if torch.cuda.is_available() else lambda: -1
         _torch, _args = torch, checks
     return _torch
 
 
-def _raw_stream(stream) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
+def _raw_stream(device: int, stream) -> int:
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
+        raise SpecError(f"the stream is on cuda:{stream.device_index}, the call on cuda:{device}")
+    return stream.cuda_stream
 
 
 def _cache_shape(cache, D: int) -> tuple:
@@ -528,14 +532,15 @@ def spec_block_tables(seq_len, accept_len, new_len, num_blocks, ring_pos, free_r
     B, table, rows, ring = b[0], tuple(block_table.shape), tuple(slots.shape), tuple(free_ring.shape)
     if len(b) != 1 or len(table) != 2 or len(rows) != 1 or len(ring) != 1 or table[0] != B:
         raise SpecError("seq_len, slots and free_ring must be vectors, block_table [B, pages]")
+    dev = _device()
     a = _TABLES.pack(B, page_size, ring[0], table[1], rows[0], *_args.addresses(
-        "seq_len", seq_len, i32, b, "accept_len?", accept_len, i32, b, "new_len", new_len, i32, b,
+        dev, "seq_len", seq_len, i32, b, "accept_len?", accept_len, i32, b, "new_len", new_len, i32, b,
         "num_blocks", num_blocks, i32, b, "ring_pos", ring_pos, i64, (2,), "free_ring", free_ring, i32, ring,
         "block_table", block_table, i32, table, "seq_len_out", seq_len_out, i32, b, "kv_len", kv_len, i32, b,
         "num_blocks_out", num_blocks_out, i32, b, "ring_pos_out", ring_pos_out, i64, (2,),
         "row_ptr", row_ptr, i32, (B + 1,), "slots", slots, i32, rows, "positions", positions, i32, rows,
         "dev_status", dev_status, i32, (4,)))
-    rc = lib().spec_block_tables(a, _raw_stream(stream))
+    rc = lib().spec_block_tables(a, _raw_stream(dev, stream))
     if rc:
         _check(rc, "spec_block_tables")
 
@@ -552,13 +557,14 @@ def spec_cache_append(k, v, slots, cache, dev_status, k_scale: float = 1.0, v_sc
     pages, Hkv, P = _cache_shape(cache, D)
     if Hkv != H or v.dtype is not k.dtype:
         raise SpecError(f"k, v and cache disagree: {H} and {Hkv} heads, {k.dtype} and {v.dtype}")
+    dev = _device()
     kp, kr, kh, vp, vr, vh, sp, cp, ks, vs, st = _args.addresses(
-        "k", k, None, shape, "v", v, None, shape, "slots", slots, T.int32, (rows,),
+        dev, "k", k, None, shape, "v", v, None, shape, "slots", slots, T.int32, (rows,),
         "cache", cache, T.uint8, (pages, H, P // 16, 18 * D), "k_stored?", k_stored, k.dtype, shape,
         "v_stored?", v_stored, k.dtype, shape, "dev_status", dev_status, T.int32, (4,))
     a = _APPEND.pack(rows, H, D, _storage(k), P, pages, kp, vp, kr, kh, vr, vh, sp, k_scale, v_scale, cp,
                      ks, vs, st)
-    rc = lib().spec_cache_append(a, _raw_stream(stream))
+    rc = lib().spec_cache_append(a, _raw_stream(dev, stream))
     if rc:
         _check(rc, "spec_cache_append")
 
@@ -582,15 +588,16 @@ def spec_cache_attention(q, cache, block_table, kv_len, row_ptr, out, dev_status
     B = table[0]
     pages, Hkv, P = _cache_shape(cache, D)
     words = 0 if tree_mask is None else tree_mask.shape[1]
-    qp, qr, qh, cp, tp, lp, rp, mp, op, ep, st = _args.addresses(
-        "q", q, None, shape, "cache", cache, T.uint8, (pages, Hkv, P // 16, 18 * D),
+    dev = _device()
+    qp, qr, qh, cp, tp, lp, rp, mp, op, ep, st, wp, wn = _args.addresses(
+        dev, "q", q, None, shape, "cache", cache, T.uint8, (pages, Hkv, P // 16, 18 * D),
         "block_table", block_table, i32, table, "kv_len", kv_len, i32, (B,), "row_ptr", row_ptr, i32, (B + 1,),
         "tree_mask?", tree_mask, i32, (rows, words), "out", out, q.dtype, shape, "lse?", lse, T.float32, (rows, Hq),
-        "dev_status", dev_status, i32, (4,))
+        "dev_status", dev_status, i32, (4,), "workspace", workspace, None, None)
     a = _ATTENTION.pack(
         B, rows, Hq, Hkv, D, _storage(q), P, pages, table[1], words, qp, qr, qh, cp, tp, lp, rp, mp,
-        softmax_scale, k_scale, v_scale, op, ep, st, _ptr(workspace), workspace.nbytes)
-    rc = lib().spec_cache_attention(a, _raw_stream(stream))
+        softmax_scale, k_scale, v_scale, op, ep, st, wp, wn)
+    rc = lib().spec_cache_attention(a, _raw_stream(dev, stream))
     if rc:
         _check(rc, "spec_cache_attention")
 
@@ -605,20 +612,21 @@ def spec_logprobs(logits, tokens, logprob, entropy, dev_status, workspace, tempe
     and the K = top_ids.shape[2] largest entries of each row."""
     T = _types()
     f32, i32 = T.float32, T.int32
-    shape, s = tuple(logits.shape), logits.stride()
-    if len(shape) != 3 or s[2] != 1 or not logits.is_cuda:
-        raise SpecError("logits must be a CUDA tensor [B, n, V] with contiguous rows")
+    shape = tuple(logits.shape)
+    if len(shape) != 3:
+        raise SpecError(f"logits must be [B, n, V], not {list(shape)}")
     if (top_ids is None) != (top_logprobs is None):
         raise SpecError("top_ids and top_logprobs go together")
     B, n, V = shape
     K = 0 if top_ids is None else top_ids.shape[2]
-    tp, Tp, lp, ep, ip, kp, st = _args.addresses(
-        "tokens", tokens, i32, (B, n), "temperature?", temperature, f32, (B,), "logprob", logprob, f32, (B, n),
+    dev = _device()
+    xp, xb, xr, tp, Tp, lp, ep, ip, kp, st, wp, wn = _args.addresses(
+        dev, "logits", logits, None, shape, "tokens", tokens, i32, (B, n), "temperature?", temperature, f32, (B,), "logprob", logprob, f32, (B, n),
         "entropy", entropy, f32, (B, n), "top_ids?", top_ids, i32, (B, n, K),
-        "top_logprobs?", top_logprobs, f32, (B, n, K), "dev_status", dev_status, i32, (4,))
+        "top_logprobs?", top_logprobs, f32, (B, n, K), "dev_status", dev_status, i32, (4,),
+        "workspace", workspace, None, None)
     a = _LOGPROBS.pack(
-        B, n, V, K, _storage(logits), logits.data_ptr(), s[0], s[1], tp, Tp, lp, ep, ip if K else 0,
-        kp if K else 0, st, _ptr(workspace), workspace.nbytes)
-    rc = lib().spec_logprobs(a, _raw_stream(stream))
+        B, n, V, K, _storage(logits), xp, xb, xr, tp, Tp, lp, ep, ip if K else 0, kp if K else 0, st, wp, wn)
+    rc = lib().spec_logprobs(a, _raw_stream(dev, stream))
     if rc:
         _check(rc, "spec_logprobs")

@@ -4,10 +4,12 @@
 //
 //   built_for                       the torch whose objects this reads
 //   use(error)                      the exception that refusals raise
-//   addresses(what, t, dtype, shape, ...)  four arguments a tensor; the addresses
-//       of contiguous CUDA tensors of these types and shapes.  dtype None: heads
-//       contiguous, any dtype; address, row stride, head stride of [T][H][D].
-//       t None: 0 where `what` ends in '?', else refused.
+//   addresses(device, what, t, dtype, shape, ...)  four arguments a tensor; the
+//       addresses of contiguous tensors of these types and shapes on that CUDA
+//       device.  dtype None: any dtype, the last dimension contiguous; address and
+//       the two other strides of [T][H][D].  dtype and shape None: any contiguous
+//       tensor; address and bytes.  t None: 0 where `what` ends in '?', else
+//       refused.
 #include <c10/core/ScalarType.h>
 #include <c10/util/Exception.h>
 #include <torch/csrc/Dtype.h>
@@ -60,8 +62,13 @@ PyObject* checked_addresses(PyObject* const* a, Py_ssize_t n) {
   constexpr Py_ssize_t MOST = 64;
   long long out[MOST];
   Py_ssize_t m = 0;
-  if (n % 4 != 0) return refuse("four arguments a tensor");
-  for (Py_ssize_t i = 0; i < n; i += 4) {
+  if (n % 4 != 1) return refuse("a device and four arguments a tensor");
+  const long device = PyLong_AsLong(a[0]);
+  if (device == -1 && PyErr_Occurred()) return nullptr;
+  auto elsewhere = [&](PyObject* what, const at::Tensor& x) {
+    return refuse(text(what) + " is on " + x.device().str() + ", the call on cuda:" + std::to_string(device));
+  };
+  for (Py_ssize_t i = 1; i < n; i += 4) {
     if (m + 3 > MOST) return refuse("too many tensors");
     PyObject *what = a[i], *t = a[i + 1], *dtype = a[i + 2], *shape = a[i + 3];
     if (t == Py_None) {
@@ -72,14 +79,22 @@ PyObject* checked_addresses(PyObject* const* a, Py_ssize_t n) {
     }
     if (!THPVariable_Check(t)) return refuse(text(what) + " must be a tensor");
     const at::Tensor& x = THPVariable_Unpack(t);
-    if (dtype == Py_None) {
+    if (dtype == Py_None && shape != Py_None) {
       if (!same_shape(x.sizes(), shape) || x.dim() != 3 || x.stride(2) != 1)
-        return refuse(text(what) + " must be " + text(shape) + " with contiguous heads, not " + list_of(x.sizes()) +
+        return refuse(text(what) + " must be " + text(shape) + " with a contiguous last dimension, not " + list_of(x.sizes()) +
                       " with strides " + list_of(x.strides()));
       if (!x.is_cuda()) return refuse(text(what) + " must be a CUDA tensor");
+      if (x.device().index() != device) return elsewhere(what, x);
       out[m++] = (long long)(uintptr_t)x.data_ptr();
       out[m++] = x.stride(0);
       out[m++] = x.stride(1);
+      continue;
+    }
+    if (dtype == Py_None) {
+      if (!x.is_cuda() || !x.is_contiguous()) return refuse(text(what) + " must be a contiguous CUDA tensor");
+      if (x.device().index() != device) return elsewhere(what, x);
+      out[m++] = (long long)(uintptr_t)x.data_ptr();
+      out[m++] = (long long)x.nbytes();
       continue;
     }
     if (!THPDtype_Check(dtype)) return refuse("a dtype is expected for " + text(what));
@@ -87,6 +102,7 @@ PyObject* checked_addresses(PyObject* const* a, Py_ssize_t n) {
       return refuse(text(what) + " must be " + text(dtype) + " " + text(shape) + ", not " + c10::toString(x.scalar_type()) +
                     " " + list_of(x.sizes()));
     if (!x.is_cuda() || !x.is_contiguous()) return refuse(text(what) + " must be a contiguous CUDA tensor");
+    if (x.device().index() != device) return elsewhere(what, x);
     out[m++] = (long long)(uintptr_t)x.data_ptr();
   }
   PyObject* r = PyTuple_New(m);

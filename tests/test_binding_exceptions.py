@@ -15,7 +15,7 @@ build.build()
 _lib._types()
 def addresses(*a):
     try:
-        _lib._args.addresses(*a)
+        _lib._args.addresses(-1, *a)
     except _lib.SpecError as e:
         print("refused:", e)
 """
