@@ -529,9 +529,10 @@ def spec_block_tables(seq_len, accept_len, new_len, num_blocks, ring_pos, free_r
     T = _types()
     i32, i64 = T.int32, T.int64
     b = tuple(seq_len.shape)
-    B, table, rows, ring = b[0], tuple(block_table.shape), tuple(slots.shape), tuple(free_ring.shape)
-    if len(b) != 1 or len(table) != 2 or len(rows) != 1 or len(ring) != 1 or table[0] != B:
+    table, rows, ring = tuple(block_table.shape), tuple(slots.shape), tuple(free_ring.shape)
+    if len(b) != 1 or len(table) != 2 or len(rows) != 1 or len(ring) != 1 or table[0] != b[0]:
         raise SpecError("seq_len, slots and free_ring must be vectors, block_table [B, pages]")
+    B = b[0]
     dev = _device()
     a = _TABLES.pack(B, page_size, ring[0], table[1], rows[0], *_args.addresses(
         dev, "seq_len", seq_len, i32, b, "accept_len?", accept_len, i32, b, "new_len", new_len, i32, b,
@@ -587,6 +588,8 @@ def spec_cache_attention(q, cache, block_table, kv_len, row_ptr, out, dev_status
     rows, Hq, D = shape
     B = table[0]
     pages, Hkv, P = _cache_shape(cache, D)
+    if tree_mask is not None and tree_mask.dim() != 2:
+        raise SpecError(f"tree_mask must be [T, words], not {list(tree_mask.shape)}")
     words = 0 if tree_mask is None else tree_mask.shape[1]
     dev = _device()
     qp, qr, qh, cp, tp, lp, rp, mp, op, ep, st, wp, wn = _args.addresses(
@@ -618,6 +621,8 @@ def spec_logprobs(logits, tokens, logprob, entropy, dev_status, workspace, tempe
     if (top_ids is None) != (top_logprobs is None):
         raise SpecError("top_ids and top_logprobs go together")
     B, n, V = shape
+    if top_ids is not None and top_ids.dim() != 3:
+        raise SpecError(f"top_ids must be [B, n, K], not {list(top_ids.shape)}")
     K = 0 if top_ids is None else top_ids.shape[2]
     dev = _device()
     xp, xb, xr, tp, Tp, lp, ep, ip, kp, st, wp, wn = _args.addresses(
