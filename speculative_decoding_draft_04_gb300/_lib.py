@@ -467,6 +467,15 @@ def _format(py) -> struct.Struct:
 
 _TABLES, _APPEND = _format(BlockTablesArgs), _format(CacheAppendArgs)
 _ATTENTION, _LOGPROBS = _format(CacheAttentionArgs), _format(LogprobsArgs)
+
+
+def _pack(fmt: struct.Struct, *values) -> bytes:
+    try:
+        return fmt.pack(*values)
+    except struct.error as e:
+        raise SpecError(f"an argument does not fit its C type: {e}") from e
+
+
 _torch = _args = None
 _device = None              # the current device: launches go to it, so every tensor and the stream have to be on it
 
@@ -534,7 +543,7 @@ def spec_block_tables(seq_len, accept_len, new_len, num_blocks, ring_pos, free_r
         raise SpecError("seq_len, slots and free_ring must be vectors, block_table [B, pages]")
     B = b[0]
     dev = _device()
-    a = _TABLES.pack(B, page_size, ring[0], table[1], rows[0], *_args.addresses(
+    a = _pack(_TABLES, B, page_size, ring[0], table[1], rows[0], *_args.addresses(
         dev, "seq_len", seq_len, i32, b, "accept_len?", accept_len, i32, b, "new_len", new_len, i32, b,
         "num_blocks", num_blocks, i32, b, "ring_pos", ring_pos, i64, (2,), "free_ring", free_ring, i32, ring,
         "block_table", block_table, i32, table, "seq_len_out", seq_len_out, i32, b, "kv_len", kv_len, i32, b,
@@ -563,8 +572,8 @@ def spec_cache_append(k, v, slots, cache, dev_status, k_scale: float = 1.0, v_sc
         dev, "k", k, None, shape, "v", v, None, shape, "slots", slots, T.int32, (rows,),
         "cache", cache, T.uint8, (pages, H, P // 16, 18 * D), "k_stored?", k_stored, k.dtype, shape,
         "v_stored?", v_stored, k.dtype, shape, "dev_status", dev_status, T.int32, (4,))
-    a = _APPEND.pack(rows, H, D, _storage(k), P, pages, kp, vp, kr, kh, vr, vh, sp, k_scale, v_scale, cp,
-                     ks, vs, st)
+    a = _pack(_APPEND, rows, H, D, _storage(k), P, pages, kp, vp, kr, kh, vr, vh, sp, k_scale, v_scale, cp,
+              ks, vs, st)
     rc = lib().spec_cache_append(a, _raw_stream(dev, stream))
     if rc:
         _check(rc, "spec_cache_append")
@@ -597,9 +606,8 @@ def spec_cache_attention(q, cache, block_table, kv_len, row_ptr, out, dev_status
         "block_table", block_table, i32, table, "kv_len", kv_len, i32, (B,), "row_ptr", row_ptr, i32, (B + 1,),
         "tree_mask?", tree_mask, i32, (rows, words), "out", out, q.dtype, shape, "lse?", lse, T.float32, (rows, Hq),
         "dev_status", dev_status, i32, (4,), "workspace", workspace, None, None)
-    a = _ATTENTION.pack(
-        B, rows, Hq, Hkv, D, _storage(q), P, pages, table[1], words, qp, qr, qh, cp, tp, lp, rp, mp,
-        softmax_scale, k_scale, v_scale, op, ep, st, wp, wn)
+    a = _pack(_ATTENTION, B, rows, Hq, Hkv, D, _storage(q), P, pages, table[1], words, qp, qr, qh, cp, tp, lp,
+              rp, mp, softmax_scale, k_scale, v_scale, op, ep, st, wp, wn)
     rc = lib().spec_cache_attention(a, _raw_stream(dev, stream))
     if rc:
         _check(rc, "spec_cache_attention")
@@ -630,8 +638,8 @@ def spec_logprobs(logits, tokens, logprob, entropy, dev_status, workspace, tempe
         "entropy", entropy, f32, (B, n), "top_ids?", top_ids, i32, (B, n, K),
         "top_logprobs?", top_logprobs, f32, (B, n, K), "dev_status", dev_status, i32, (4,),
         "workspace", workspace, None, None)
-    a = _LOGPROBS.pack(
-        B, n, V, K, _storage(logits), xp, xb, xr, tp, Tp, lp, ep, ip if K else 0, kp if K else 0, st, wp, wn)
+    a = _pack(_LOGPROBS, B, n, V, K, _storage(logits), xp, xb, xr, tp, Tp, lp, ep, ip if K else 0,
+              kp if K else 0, st, wp, wn)
     rc = lib().spec_logprobs(a, _raw_stream(dev, stream))
     if rc:
         _check(rc, "spec_logprobs")

@@ -1,5 +1,5 @@
-"""Tensors of the wrong number of dimensions are refused with SpecError by the serving calls, not with
-whatever indexing raises."""
+"""Tensors of the wrong number of dimensions and numbers that do not fit the C types are refused with
+SpecError by the serving calls, not with whatever indexing or packing raises."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -12,6 +12,21 @@ st = torch.zeros(4, dtype=i32)
 @pytest.fixture(scope="module", autouse=True)
 def built():
     build.build()
+
+
+@pytest.fixture
+def packed(monkeypatch):
+    """Checks that find every tensor in place, so that only the numbers are left."""
+    class Checks:
+        @staticmethod
+        def addresses(dev, *a):
+            out = []
+            for _, _, dtype, shape in zip(*[iter(a)] * 4):
+                out += [0] * (1 if dtype is not None else 2 if shape is None else 3)
+            return tuple(out)
+    _lib._types()
+    monkeypatch.setattr(_lib, "_args", Checks)
+    monkeypatch.setattr(_lib, "_raw_stream", lambda device, stream: 0)   # the library refuses infinite scales itself
 
 
 def tables(seq_len=torch.zeros(2, dtype=i32), page_size=16):
@@ -52,3 +67,11 @@ def test_dimensions_of_the_alternatives(shape):
 def test_dimensions_of_lengths(shape):
     with pytest.raises(_lib.SpecError, match="seq_len"):
         tables(torch.zeros(shape, dtype=i32))
+
+
+def test_numbers_that_do_not_fit(packed):
+    for call in (lambda: tables(page_size=2 ** 31), lambda: tables(page_size=16.5), lambda: tables(page_size=None),
+                 lambda: attention(softmax_scale=1e39), lambda: attention(k_scale="1"),
+                 lambda: append(k_scale=-1e300), lambda: append(v_scale=None)):
+        with pytest.raises(_lib.SpecError):
+            call()
