@@ -67,6 +67,7 @@ cudaError_t launch_tree_verify(const TreeShape&, const void*, const void*, const
 cudaError_t launch_block_tables(const spec_block_tables_args&, int, cudaStream_t);
 cudaError_t launch_cache_append(const spec_cache_append_args&, int, cudaStream_t);
 size_t cache_attention_workspace_bytes(int, int, int);
+float cache_attention_scale(const spec_cache_attention_args&);
 cudaError_t launch_cache_attention(const spec_cache_attention_args&, int, cudaStream_t);
 size_t logprobs_workspace_bytes(int, int, int);
 cudaError_t launch_logprobs(const spec_logprobs_args&, int, cudaStream_t);
@@ -831,8 +832,8 @@ int32_t spec_cache_attention(const spec_cache_attention_args* a, spec_stream_t s
   if (a->B < 1 || a->B > 4096 || a->T < 0 || a->T >= (1 << 24) || a->Hkv < 1 || a->Hq < a->Hkv ||
       a->Hq > 256 || a->Hq % a->Hkv != 0 || (int64_t)a->T * a->Hq > 0x7fffffff || a->num_pages < 1 || a->table_stride < 1 ||
       (int64_t)a->B * a->table_stride > 0x7fffffff || (int64_t)a->num_pages * a->page_size > 0x7fffffff ||
-      !cache_scale_ok(a->k_scale) || !cache_scale_ok(a->v_scale) || !isfinite(a->softmax_scale) ||
-      a->mask_words < 0 || (a->tree_mask && a->mask_words < 1))
+      !cache_scale_ok(a->k_scale) || !cache_scale_ok(a->v_scale) ||
+      !isfinite(cache_attention_scale(*a)) || a->mask_words < 0 || (a->tree_mask && a->mask_words < 1))
     return SPEC_EINVAL;
   if (!page_ok(a->page_size) || !head_ok(a->D) || (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16))
     return SPEC_EUNSUPPORTED;

@@ -793,11 +793,16 @@ size_t cache_attention_workspace_bytes(int Hq, int Hkv, int D) {
   return (size_t)AT_MAX_CTAS * AT_WARPS * sizeof(AttnSplit) + parts * AT_WARPS * 2 * part + 256;
 }
 
+// What scores in codes are multiplied by.
+float cache_attention_scale(const spec_cache_attention_args& a) {
+  return a.softmax_scale * a.k_scale * 1.4426950408889634f;
+}
+
 cudaError_t launch_cache_attention(const spec_cache_attention_args& a, int sms, cudaStream_t st) {
   const int G = a.Hq / a.Hkv;
   AttnParams p{a.B, a.T, a.Hq, a.Hkv, G, a.page_size, a.num_pages, a.table_stride, a.mask_words, a.q, a.q_row_stride,
                a.q_head_stride, a.cache, a.block_table, a.kv_len, a.row_ptr, a.tree_mask,
-               a.softmax_scale * a.k_scale * 1.4426950408889634f, a.v_scale, a.out, a.lse, a.dev_status, a.workspace};
+               cache_attention_scale(a), a.v_scale, a.out, a.lse, a.dev_status, a.workspace};
   // Tiles of 8 rows where the mean request has no more: one token of 32
   // requests (4 query heads a key-value head, 265k tokens held) takes 91 us in
   // them and 107 us in 16-row tiles.  Else 16-row tiles (12 warps of 168 registers), but
