@@ -324,8 +324,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_attention_join_kernel(cons
             o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (x <= s.last) {
               const float* part = parts + (size_t)(2 * x + (x == s.first ? 1 : 0)) * PART;
-              v[k] = __ldg(reinterpret_cast<const float2*>(part + ROWS * D + 2 * rl));
-              o[k] = __ldg(reinterpret_cast<const float4*>(part + rl * D + d));
+              // not by the read-only path: the parts were written while this kernel was there
+              v[k] = __ldcg(reinterpret_cast<const float2*>(part + ROWS * D + 2 * rl));
+              o[k] = __ldcg(reinterpret_cast<const float4*>(part + rl * D + d));
             }
           }
 #pragma unroll
