@@ -509,7 +509,8 @@ int32_t spec_block_tables(const spec_block_tables_args* args, spec_stream_t stre
  * group's largest level under the largest scale, both with SPEC_DEV_BAD_KV.
  * k_stored / v_stored (optional) receive the values as stored, in dtype,
  * zeros for skipped rows.  A slot outside the cache sets SPEC_DEV_BAD_SLOT and
- * its row is skipped; two rows with one slot leave either's token there.
+ * its row is skipped; two rows with one slot leave parts of both there (groups,
+ * codes and scales are written apart).
  * k, v: rows of Hkv heads of D elements, row and head strides in elements
  * (multiples of 8 for bf16, of 4 for fp32).  1 <= Hkv <= 256, 0 <= T < 2^24,
  * (T + 16) Hkv D < 2^36.                                                    */
