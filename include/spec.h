@@ -456,8 +456,8 @@ size_t spec_cache_bytes(int32_t num_pages, int32_t Hkv, int32_t page_size, int32
  * launch.  Request b keeps base = seq_len + accept_len + 1 tokens (accept_len
  * as spec_verify wrote it; -1 keeps nothing new, and is what a request that
  * had no rows in the last block must be given; a NULL accept_len array keeps
- * seq_len) and appends new_len tokens; new_len = -1 is a finished
- * request, which keeps nothing.  kv_len = base + new_len tokens need
+ * seq_len) and appends new_len tokens; new_len = -1 is a finished request,
+ * which keeps nothing.  kv_len = base + new_len tokens need
  * ceil(kv_len / page_size) pages: missing ones are taken from the ring of
  * free pages in request order, surplus ones go back to it in request order.
  * The ring holds the free pages at entries head .. tail - 1 (mod num_pages);
@@ -473,6 +473,12 @@ size_t spec_cache_bytes(int32_t num_pages, int32_t Hkv, int32_t page_size, int32
  * back (requests keep them), and ring_pos_out is ring_pos.  If free and given
  * pages are more than num_pages together, none is given back either, with the
  * same bit.
+ * Blocks are chains here: the tokens kept of one are its first.  The accepted
+ * path of a tree lies scattered over its block's rows, and the accept_len of
+ * spec_tree_verify would keep rejected nodes' keys and values, which no status
+ * bit shows.  After a block that was a tree (tree_mask below; the words are the
+ * caller's, from the parents) accept_len is -1, and the next block begins with
+ * the accepted path's tokens.
  * Row i of the packed rows (request order, row_ptr) is token positions[i] of
  * its request at slot slots[i]; rows from row_ptr[B] to max_rows get -1.
  * Table entries at and beyond num_blocks_out are left as they are, so a call

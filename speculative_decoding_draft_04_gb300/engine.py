@@ -382,7 +382,10 @@ def make_room(c: DeviceCache, new_len, accept_len=None, stream=None) -> None:
     request's new_len next tokens.  accept_len counts the kept tokens of the
     last block beyond its first (prompt length - 1 after a prompt), -1 where
     the request had no rows in it (see drop_absent); None keeps nothing of it,
-    as before the first block."""
+    as before the first block.  Kept tokens are the block's first ones, so
+    after a tree (attend's tree_mask), whose accepted path lies scattered over
+    it, keep nothing (None, or -1 for the request) and begin the next block
+    with the path's tokens."""
     old, new = c.newest, 1 - c.newest
     _lib.spec_block_tables(c.seq_len[old], accept_len, new_len, c.num_blocks[old], c.ring_pos[old],
                            c.free_ring, c.block_table, c.seq_len[new], c.kv_len, c.num_blocks[new],
