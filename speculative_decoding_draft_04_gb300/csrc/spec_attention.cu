@@ -667,15 +667,17 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
 
     long long pos = begin;
     AttnSeg next_sg = locate(begin);
-    while (pos < end && !timed_out) {
+    while (pos < end) {
       const AttnSeg sg = next_sg;
       const int u_first = sg.u;
       const int u_end = sg.nu - sg.u < end - pos ? sg.nu : sg.u + (int)(end - pos);
       const int rows = sg.n * p.G;
       C tile;
       tile.template begin<DT>(p, sg, s_q, lane);
-      bool poison = sg.bad;                              // a page outside the cache in this part
-      if (!sg.bad) {
+      // a page outside the cache in this part, or copies that never came: the
+      // share's rows are NaN from there on
+      bool poison = sg.bad || timed_out;
+      if (!poison) {
         const int tok_end = min(sg.L, u_end * AT_UNIT);
         bool bad = false;
         for (int pg = (u_first * AT_UNIT >> page_bits) + lane; pg << page_bits < tok_end; pg += 32) {
@@ -686,7 +688,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
         if (poison && lane == 0) set_status(p.status, SPEC_DEV_BAD_SLOT);
       }
 
-      for (int u = u_first; u < u_end; ++u) {
+      for (int u = u_first; u < u_end && !timed_out; ++u) {
         if (!bar_wait(bar + cstage, cphase)) timed_out = true;
         timed_out = __any_sync(0xffffffffu, timed_out);
         if (timed_out) {
