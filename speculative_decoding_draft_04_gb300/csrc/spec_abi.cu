@@ -65,12 +65,12 @@ cudaError_t launch_tree_verify(const TreeShape&, const void*, const void*, const
                                cudaStream_t);
 
 cudaError_t launch_block_tables(const spec_block_tables_args&, int, cudaStream_t);
-cudaError_t launch_cache_append(const spec_cache_append_args&, int, cudaStream_t);
+cudaError_t launch_cache_append(const spec_cache_append_args&, cudaStream_t);
 size_t cache_attention_workspace_bytes(int, int, int);
 float cache_attention_scale(const spec_cache_attention_args&);
 cudaError_t launch_cache_attention(const spec_cache_attention_args&, int, cudaStream_t);
 size_t logprobs_workspace_bytes(int, int, int);
-cudaError_t launch_logprobs(const spec_logprobs_args&, int, cudaStream_t);
+cudaError_t launch_logprobs(const spec_logprobs_args&, cudaStream_t);
 
 // ---------------------------------------------------------------- options
 namespace {
@@ -815,11 +815,9 @@ int32_t spec_cache_append(const spec_cache_append_args* a, spec_stream_t stream)
       !stride_ok(a->k_row_stride, a->dtype) || !stride_ok(a->k_head_stride, a->dtype) ||
       !stride_ok(a->v_row_stride, a->dtype) || !stride_ok(a->v_head_stride, a->dtype))
     return SPEC_EALIGN;
-  const int sms = num_sms();
-  if (sms <= 0) return SPEC_ECUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope p(st, ST_CACHE_APPEND);
-  return launch_cache_append(*a, sms, st) == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+  return launch_cache_append(*a, st) == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }
 
 size_t spec_cache_attention_workspace_bytes(int32_t Hq, int32_t Hkv, int32_t D) {
@@ -875,11 +873,9 @@ int32_t spec_logprobs(const spec_logprobs_args* a, spec_stream_t stream) {
   if (!a->workspace || a->workspace_bytes < spec_logprobs_workspace_bytes(a->B * a->n, a->V, a->K))
     return SPEC_EWORKSPACE;
   if (!aligned(a->workspace, 16)) return SPEC_EALIGN;
-  const int sms = num_sms();
-  if (sms <= 0) return SPEC_ECUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope p(st, ST_LOGPROBS);
-  return launch_logprobs(*a, sms, st) == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+  return launch_logprobs(*a, st) == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }
 
 // ---------------------------------------------------------------- trees

@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) cache_append_kernel(const __gr
   }
 }
 
-cudaError_t launch_cache_append(const spec_cache_append_args& a, int sms, cudaStream_t st) {
+cudaError_t launch_cache_append(const spec_cache_append_args& a, cudaStream_t st) {
   AppendParams p{};
   p.T = a.T; p.Hkv = a.Hkv; p.D = a.D; p.P = a.page_size; p.bpp = a.page_size / CACHE_BLOCK;
   p.num_slots = a.num_pages * a.page_size;

@@ -104,7 +104,7 @@ __device__ __forceinline__ uint32_t bits_of(float x) { return __float_as_uint(x)
 // The vector of elements [at, at + E) of a row of V, -inf where there is none.
 template <class DT>
 __device__ __noinline__ uint4 edge_vector(const DT* x, int at, int V) {
-  constexpr int E = 16 / sizeof(DT), PER = 4 / sizeof(DT);
+  constexpr int PER = 4 / sizeof(DT);
   const uint32_t w = neg_inf_word(static_cast<const DT*>(nullptr));
   uint32_t o[4];
 #pragma unroll
@@ -116,7 +116,6 @@ __device__ __noinline__ uint4 edge_vector(const DT* x, int at, int V) {
       if (v >= 0 && v < V) o[i] = PER == 1 ? bits_of(x[v]) : e ? (o[i] & 0xffffu) | bits_of(x[v]) << 16 : (o[i] & 0xffff0000u) | bits_of(x[v]);
     }
   }
-  (void)E;
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -556,7 +555,7 @@ static cudaError_t launch(LogprobParams p, const spec_logprobs_args& a, cudaStre
   return cudaLaunchKernelEx(&cfg, logprobs_join_kernel<DT>, p);
 }
 
-cudaError_t launch_logprobs(const spec_logprobs_args& a, int sms, cudaStream_t st) {
+cudaError_t launch_logprobs(const spec_logprobs_args& a, cudaStream_t st) {
   LogprobParams p{a.B, a.n, a.V, a.K, 0, 0.f, a.logits, a.b_stride, a.row_stride, a.tokens, a.temperature, a.logprob,
                   a.entropy, a.top_ids, a.top_logprobs, a.dev_status, nullptr, nullptr};
   return a.dtype == SPEC_BF16 ? launch<bf16>(p, a, st) : launch<float>(p, a, st);
