@@ -293,7 +293,7 @@ cudaError_t launch_block_tables(const spec_block_tables_args& a, int sms, cudaSt
   if (ctas < 1) ctas = 1;
   if (ctas > sms) ctas = sms;
   const size_t smem = (size_t)5 * (a.B + 1) * sizeof(int);
-  if (smem > 48 * 1024) {
+  if (smem > 47 * 1024) {                   // 48 KB less the static arrays need no asking
     const cudaError_t e = cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)smem);
     if (e != cudaSuccess) return e;
