@@ -34,10 +34,11 @@
 //
 // Bound by instructions, not bytes: a token of one head (144 bytes at D = 128)
 // costs a warp's pass 22 instructions, 12 of them to decode it, at 2.1 a cycle
-// and SM.  One token of 32 requests (306 MB) takes 75 us, 4.1 TB/s of the 6.8 of
-// a copy; blocks of 1 to 8 tokens and 4 heads for 128 requests (619 MB) 272 us;
-// the same for 4 requests of 50k to 131k tokens (418 MB) 134 us.  Twelve warps of
-// 168 registers were faster than eight of 255 (290 against 312 us on the blocks).
+// and SM.  One token of 32 requests (306 MB) takes 74 us, 4.1 TB/s of the 6.8 of
+// a copy; blocks of 2 to 8 tokens and 4 heads for 128 requests (619 MB) 255 to
+// 290 us, by their lengths; the same for 4 requests of 50k to 131k tokens (418 MB)
+// 131 to 151 us.  Twelve warps of 168 registers were faster than eight of 255 (by
+// 7 % on the blocks when they were chosen).
 //
 // A segment inside one warp's share is written at once.  Otherwise each part is
 // kept as (m, sum, unnormalised out) in the workspace and
@@ -805,12 +806,19 @@ cudaError_t launch_cache_attention(const spec_cache_attention_args& a, int sms, 
   AttnParams p{a.B, a.T, a.Hq, a.Hkv, G, a.page_size, a.num_pages, a.table_stride, a.mask_words, a.q, a.q_row_stride,
                a.q_head_stride, a.cache, a.block_table, a.kv_len, a.row_ptr, a.tree_mask,
                cache_attention_scale(a), a.v_scale, a.out, a.lse, a.dev_status, a.workspace};
-  // Tiles of 8 rows where the mean request has no more: one token of 32
-  // requests (4 query heads a key-value head, 265k tokens held) takes 91 us in
-  // them and 107 us in 16-row tiles.  Else 16-row tiles (12 warps of 168 registers), but
-  // 32-row tiles (8 warps of 255) where the mean request nearly fills one: 4 x
-  // 90k tokens take 237 us in two 16-row tiles and 199 us in one of 32; with 8 to
-  // 32 rows a request (mean 20) 128 x 4k tokens take 290 and 305 us.
+  // The tile by the mean rows a request (finished requests and rows of no request
+  // count in it: the host does not see them).  Times are us a call of these
+  // kernels, cold caches, D = 128, 4 query heads a key-value head, all requests of
+  // one number of rows: (a) 32 requests of 64 to 4096 tokens, (b) 128 of 64 to
+  // 8192, (c) 4 of 50k to 131k; D = 64 orders them nearly alike.
+  //   8-row tiles up to 8:  8 rows take (a) 44, (b) 141, (c) 105 in them and 48,
+  //     174, 115 in 16-row tiles; 12 rows 56, 250, 158 and 52, 188, 118.  fp32 and
+  //     D = 256, 4 rows of 32 requests to 16384 tokens: 77 to 95 and 87 to 149.
+  //   32-row tiles from a mean above 24 to 32:  28 rows (b) 304, (c) 169 in one
+  //     and 350, 196 in two 16-row tiles.  (a) loses, 82 against 77.  Uniform
+  //     requests of 20 rows would gain too (280 against 328, 166 against 191), but
+  //     blocks of mixed sizes hardly do (b, 8 to 32 rows: 256 against 268) or lose
+  //     (c, 8 to 20 rows: 165 against 131).
   const long long rows = (long long)a.T * G;
   const bool few = rows <= 8LL * a.B, wide = rows > 24LL * a.B && rows <= 32LL * a.B;
   if (a.dtype == SPEC_F32) {
@@ -819,9 +827,10 @@ cudaError_t launch_cache_attention(const spec_cache_attention_args& a, int sms, 
       return few ? launch_cfg<ColumnTile<128, 2>, float>(p, sms, st) : launch_cfg<RowTiles<128, 1, 2>, float>(p, sms, st);
     return few ? launch_cfg<ColumnTile<256, 2>, float>(p, sms, st) : launch_cfg<RowTiles<256, 1, 2>, float>(p, sms, st);
   }
-  // above a mean of 32 rows, 128-row tiles: 34 rows of 128 x 4k tokens take 406 us
-  // in them and in 16-row tiles, 50 rows 418 and 570; trees of 100 rows over 32 x
-  // 2k 126 and 265
+  //   128-row tiles above 32:  36 rows take (a) 66, (b) 357, (c) 224 in them, 97,
+  //     492, 274 in 16-row tiles and 122, 533, 286 in 32-row tiles; 100 rows 75,
+  //     379, 235 against 211, 1120, 596.  At 32 rows (b) 347, (c) 219 lose to 305
+  //     and 170, and only (a) would gain (64 against 83).
   if (a.D <= 128 && rows > 32LL * a.B) return launch_cache_attention_tc(p, a.D, sms, st);
   if (a.D == 64)
     return few    ? launch_cfg<ColumnTile<64, 1>, bf16>(p, sms, st)

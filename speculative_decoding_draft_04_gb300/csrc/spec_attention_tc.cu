@@ -22,13 +22,15 @@
 // kernels of smaller tiles, but a segment counts four units more: beginning and
 // ending one (queries in, outputs out, an empty pipeline) takes as long as that,
 // and short requests' segments would otherwise meet in one CTA (trees of 100 rows
-// over 32 requests of 25 to 4096 tokens: 119 us, with the lead 85, cold caches).
+// over 32 requests of 25 to 4096 tokens: 119 us without it and with keys' and
+// values' buffers taken together, 75 now).
 //
 // Bound by the chain of waits from step to step of a unit: 3500 cycles a unit
 // and CTA, two CTAs at a time, of which the products are some 500 a unit.  The
 // trees keep 42 % of the issue slots, 27 % of the tensor pipe and 19 % of the
-// memory busy.  100 of 128 rows reach 0.4 PFLOP/s (75 us a call); 16-row tiles of
-// mma.sync took 265 us for the same trees, decoding every token seven times.
+// memory busy.  100 of 128 rows reach 0.4 PFLOP/s (72 to 80 us a call, by the
+// trees' lengths); 16-row tiles of mma.sync take 211 us for as many rows, decoding
+// every token seven times.  Eight prompts of 512 tokens take 102 us, of 2048 777.
 #include <atomic>
 
 #include "spec_attention.cuh"

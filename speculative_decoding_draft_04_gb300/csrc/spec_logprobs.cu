@@ -4,6 +4,9 @@
 //   d = (x - m) log2(e) / T,  Z = sum 2^d,  lse = m / T + ln Z
 //   logprob = (x_token - m) / T - ln Z,     H = ln 2 (log2 Z - sum 2^d d / Z)
 //
+// d is one fused multiply-add of x against the rounded m log2(e) / T; what the
+// rounding adds to every d of a warp is known exactly and leaves its sums again.
+//
 // One read of each row.  logprobs_kernel: a CTA takes one segment of one row,
 // 256 threads x 16 vectors of 16 bytes, all requested at once and kept in
 // registers, so that maximum, sums and candidates come from one load.
@@ -16,9 +19,12 @@
 //
 // Bound by latency between its phases (load, maxima, sums, bound, candidates), not
 // by bytes: 128 requests of 1 to 8 tokens and 32000 bf16 logits (37 MB) take
-// 20 us, 256 of 128256 (296 MB) 92 us, 3.2 TB/s of the 6.8 of a copy.  Two CTAs of
-// 64 KB in registers an SM overlap each other's phases; half the vectors and four
-// CTAs took 27 and 90 us (rows of two segments to join), three CTAs spilled.
+// 18.5 us, 256 of 128256 (296 MB) 90 us, 3.3 TB/s of the 6.8 of a copy.  Two CTAs
+// of 64 KB in registers an SM overlap each other's phases; half the vectors and
+// four CTAs took 27 and 90 us (rows of two segments to join), three CTAs spilled.
+// Warps with an entry of -inf or of the type's lowest value sum entry by entry:
+// with nine tenths of the 128256 masked 285 us.  Rows little longer than a segment
+// pay for a second one that has fewer entries than groups: 33000 entries 94 us.
 //
 // Rows of more than one segment are joined by logprobs_join_kernel, a warp a
 // row, from each segment's (m, Z, sum 2^d d) and its K sorted candidates; its

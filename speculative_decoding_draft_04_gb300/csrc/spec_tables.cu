@@ -16,9 +16,9 @@
 // call does not write, so no thread waits for another's store.
 //
 // Bound by latency: lengths, then ring and table entries, then stores, 6.3 us in
-// a graph for 128 requests of 8 rows (8.2 us a call from Python; its bytes are
+// a graph for 128 requests of 8 rows (8 us a call from Python; its bytes are
 // 10 KB).  2048 prompts with a million rows (17 MB, 2.5 us of copying) take
-// 13.7 us: instructions, the rows' bisections of 11 steps each in shared memory
+// 12.3 to 14.3 us: instructions, the rows' bisections of 11 steps each in shared memory
 // (16.4 us with divisions by the page size and a loop over the warps' sums).
 #include "spec_serve.cuh"
 
