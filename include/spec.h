@@ -556,7 +556,7 @@ int32_t spec_cache_append(const spec_cache_append_args* args, spec_stream_t stre
  * neither read nor written.  A bounded wait that gives up sets
  * SPEC_DEV_TIMEOUT.
  * softmax_scale * k_scale * log2(e) is a finite 32-bit number.
- * 1 <= B <= 4096, 0 <= T < 2^24, T * Hq < 2^31, Hq <= 256 a multiple of Hkv,
+ * 1 <= B <= 4096, 0 <= T < 2^24, T * Hq <= 2^31 - 256, Hq <= 256 a multiple of Hkv,
  * B * table_stride < 2^31, kv_len <= 2^30, q strides as in
  * spec_cache_append; workspace spec_cache_attention_workspace_bytes(Hq, Hkv,
  * D) bytes (it does not depend on the lengths), 16-byte aligned.             */

@@ -828,7 +828,8 @@ size_t spec_cache_attention_workspace_bytes(int32_t Hq, int32_t Hkv, int32_t D) 
 int32_t spec_cache_attention(const spec_cache_attention_args* a, spec_stream_t stream) {
   if (!a) return SPEC_EINVAL;
   if (a->B < 1 || a->B > 4096 || a->T < 0 || a->T >= (1 << 24) || a->Hkv < 1 || a->Hq < a->Hkv ||
-      a->Hq > 256 || a->Hq % a->Hkv != 0 || (int64_t)a->T * a->Hq > 0x7fffffff || a->num_pages < 1 || a->table_stride < 1 ||
+      a->Hq > 256 || a->Hq % a->Hkv != 0 || (int64_t)a->T * a->Hq > 0x7fffffff - 255 ||   // rows in whole tiles
+      a->num_pages < 1 || a->table_stride < 1 ||
       (int64_t)a->B * a->table_stride > 0x7fffffff || (int64_t)a->num_pages * a->page_size > 0x7fffffff ||
       !cache_scale_ok(a->k_scale) || !cache_scale_ok(a->v_scale) ||
       !isfinite(cache_attention_scale(*a)) || a->mask_words < 0 || (a->tree_mask && a->mask_words < 1))
