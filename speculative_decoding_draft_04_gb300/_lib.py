@@ -634,8 +634,8 @@ def spec_logprobs(logits, tokens, logprob, entropy, dev_status, workspace, tempe
     K = 0 if top_ids is None else top_ids.shape[2]
     dev = _device()
     xp, xb, xr, tp, Tp, lp, ep, ip, kp, st, wp, wn = _args.addresses(
-        dev, "logits", logits, None, shape, "tokens", tokens, i32, (B, n), "temperature?", temperature, f32, (B,), "logprob", logprob, f32, (B, n),
-        "entropy", entropy, f32, (B, n), "top_ids?", top_ids, i32, (B, n, K),
+        dev, "logits", logits, None, shape, "tokens", tokens, i32, (B, n), "temperature?", temperature, f32, (B,),
+        "logprob", logprob, f32, (B, n), "entropy", entropy, f32, (B, n), "top_ids?", top_ids, i32, (B, n, K),
         "top_logprobs?", top_logprobs, f32, (B, n, K), "dev_status", dev_status, i32, (4,),
         "workspace", workspace, None, None)
     a = _pack(_LOGPROBS, B, n, V, K, _storage(logits), xp, xb, xr, tp, Tp, lp, ep, ip if K else 0,

@@ -458,8 +458,8 @@ def served_cycle(d: DeviceWorkload, b: Buffers, c: DeviceCache, l: DeviceLogprob
     d.target; new_len is gamma + 1 per request (the anchor and the block), 1 +
     verify_len where lengths are scheduled.  A request that gets no rows (no
     pages for them, new_len -1 or 0) emits nothing: its accept_len and
-    out_tokens are -1, whatever d.target holds for it.  So b.accept_len of this
-    cycle is accept_len of the next for every request."""
+    out_tokens are -1, whatever finite logits d.target holds for it.  So
+    b.accept_len of this cycle is accept_len of the next for every request."""
     draft(d, b, stream)
     make_room(c, new_len, accept_len, stream)
     target_pass(d, b, c, stream)
