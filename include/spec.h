@@ -92,7 +92,9 @@ enum {
                                new tokens                                       */
   SPEC_DEV_BAD_SLOT = 512,  /* a slot or page id outside the cache              */
   SPEC_DEV_BAD_LOGIT = 1024,/* a row of logits with a NaN, +inf, or only -inf   */
-  SPEC_DEV_BAD_KV = 2048    /* a key or value to be stored that is not finite   */
+  SPEC_DEV_BAD_KV = 2048,   /* a key or value to be stored that is not finite   */
+  SPEC_DEV_BAD_FILTER = 4096,   /* a uniform number, top_p or min_p out of range */
+  SPEC_DEV_BAD_POSITION = 8192  /* a position outside the table of rotations     */
 };
 
 /* ---------------------------------------------------------------- draft */
@@ -535,6 +537,50 @@ typedef struct {
 } spec_cache_append_args;
 int32_t spec_cache_append(const spec_cache_append_args* args, spec_stream_t stream);
 
+/* spec_rotary_append: the rows of T tokens' queries, keys and values made
+ * ready for attention in one pass.  With a weight, each head x of q (k) is
+ * normed: y = (x inv) w, inv = 1 / sqrt(mean x^2 + eps) rounded to fp32, both
+ * products rounded in fp32; without one y = x.  Its first R elements are then
+ * rotated by the token's row of `rope` (pair i: c = rope[position][i][0],
+ * s = rope[position][i][1]): y_a c - y_b s and y_b c + y_a s, every product and
+ * sum rounded in fp32, where pair i is elements i and i + R / 2, or 2 i and
+ * 2 i + 1 with `interleaved`.  The result is rounded to dtype: queries go to
+ * q_out, keys (and the values, which are taken as they are) into the cache as
+ * spec_cache_append rounds them, so k_stored, v_stored and the cache are what
+ * that call leaves for the rounded keys.
+ * slots[i] = -1: row i belongs to no request; its q_out is left as it is, the
+ * values as stored are zeros.  A slot outside the cache (SPEC_DEV_BAD_SLOT) or a
+ * position outside [0, rope_rows) (SPEC_DEV_BAD_POSITION): nothing is written
+ * into the cache for the row, its q_out is NaN, the values as stored are zeros.
+ * Keys and values that are not finite are stored as in spec_cache_append
+ * (SPEC_DEV_BAD_KV).
+ * q_out may be q itself (the same address and strides); no other output may
+ * overlap an input.  Strides as in spec_cache_append, q_out's too; the limits
+ * of spec_cache_append, and 1 <= Hq <= 256, (T + 16) Hq D < 2^36, R a multiple of
+ * 32 with 32 <= R <= D, 1 <= rope_rows < 2^31, eps >= 0 and finite.  Weights
+ * are of dtype.                                                              */
+typedef struct {
+  int32_t T, Hq, Hkv, D, R, dtype;
+  int32_t page_size, num_pages, rope_rows, interleaved;
+  const void* q;              /* [T][Hq][D] by the strides                      */
+  const void* k;              /* [T][Hkv][D] by the strides                     */
+  const void* v;
+  int64_t q_row_stride, q_head_stride, k_row_stride, k_head_stride, v_row_stride, v_head_stride;
+  const void* q_weight;       /* optional [D]                                   */
+  const void* k_weight;       /* optional [D]                                   */
+  const int32_t* positions;   /* [T]                                            */
+  const int32_t* slots;       /* [T]                                            */
+  const float* rope;          /* [rope_rows][R / 2][2] cosine, sine             */
+  float eps, k_scale, v_scale;
+  void* q_out;                /* out [T][Hq][D] (dtype) by its strides          */
+  int64_t q_out_row_stride, q_out_head_stride;
+  uint8_t* cache;
+  void* k_stored;             /* optional out [T][Hkv][D] (dtype)               */
+  void* v_stored;             /* optional out [T][Hkv][D] (dtype)               */
+  uint32_t* dev_status;
+} spec_rotary_append_args;
+int32_t spec_rotary_append(const spec_rotary_append_args* args, spec_stream_t stream);
+
 /* spec_cache_attention: attention of each request's new tokens over its
  * cache, out = softmax(softmax_scale q K^T) V for every query head (query
  * head i reads key-value head i / (Hq / Hkv)).  Request b's queries are the
@@ -580,6 +626,32 @@ typedef struct {
 size_t spec_cache_attention_workspace_bytes(int32_t Hq, int32_t Hkv, int32_t D);
 int32_t spec_cache_attention(const spec_cache_attention_args* args, spec_stream_t stream);
 
+/* spec_prefix_attention: spec_cache_attention for requests of which groups
+ * begin with the same tokens, held in the cache once.  Group g is the requests
+ * group_ptr[g] .. group_ptr[g+1] - 1 (a partition of all B: group_ptr[0] = 0,
+ * group_ptr[groups] = B, ascending; empty groups are allowed), its prefix the
+ * first prefix_len[g] >= 0 tokens of the pages prefix_table[g].  Every row of the
+ * group's requests sees the whole prefix, and of the request's own tokens what
+ * spec_cache_attention says: block_table, kv_len and the masks are about those
+ * alone.  out and lse are over both; a row that sees nothing of either gets
+ * out = 0 and lse = -inf.
+ * Statuses, arithmetic and limits are those of spec_cache_attention (an entry of
+ * group_ptr or a prefix_len out of range sets SPEC_DEV_BAD_LEN, a prefix page
+ * outside the cache SPEC_DEV_BAD_SLOT: the group's rows get NaN; of a bad page
+ * at least those of its row tile).  With group_ptr's first or last entry wrong, or
+ * entries that do not ascend, every row of every request gets NaN.
+ * 0 <= groups <= 4096, groups * prefix_stride < 2^31; workspace
+ * spec_prefix_attention_workspace_bytes(T, Hq, Hkv, D) bytes.                */
+typedef struct {
+  spec_cache_attention_args own;
+  int32_t groups, prefix_stride;
+  const int32_t* prefix_table; /* [groups][prefix_stride]                        */
+  const int32_t* prefix_len;   /* [groups]                                       */
+  const int32_t* group_ptr;    /* [groups+1]                                     */
+} spec_prefix_attention_args;
+size_t spec_prefix_attention_workspace_bytes(int32_t T, int32_t Hq, int32_t Hkv, int32_t D);
+int32_t spec_prefix_attention(const spec_prefix_attention_args* args, spec_stream_t stream);
+
 /* --------------------------------------------------- log probabilities */
 /* spec_logprobs: for each row (b, j) of logits with a token >= 0, with
  * x = logits / T_b (T = 1 without temperature): logprob = x[token] - lse(x),
@@ -609,6 +681,41 @@ typedef struct {
 } spec_logprobs_args;
 size_t spec_logprobs_workspace_bytes(int32_t rows, int32_t V, int32_t K);
 int32_t spec_logprobs(const spec_logprobs_args* args, spec_stream_t stream);
+
+/* ------------------------------------------------------------- sampling */
+/* spec_sample: draws a token of each row (b, j) of logits.  With
+ * w_v = exp((x_v - max x) / T_b) and the entries in descending order (equal
+ * logits: the lower index first; -inf is no entry), the first n are kept,
+ *   n = the least of  top_k[b]                       (0 or less: no limit)
+ *                     the entries w / w_first >= min_p[b]
+ *                     the entries before which less than top_p[b] of the mass of
+ *                     the first top_k[b] lies         (1: no limit)
+ * and at least one.  The token is the smallest v with F(v) > u F(V), F summing
+ * the kept w in vocabulary order; logprob is log(w_v / F(V)), kept is n.
+ * Arithmetic: each w is a whole number of 2^-41 of the largest (2^-(62 - bits of
+ * V) for V > 2^21) within 2^-34 of its value relative, so every sum is exact, in
+ * any order: a result is the same on every run, and that of the definition unless
+ * a border is nearer than the weights' errors together, some 1e-12 of the mass.
+ * u = -1: the row is not read, its token is -1, logprob NaN, kept 0.  The same
+ * outputs, with the bit, for u outside [0, 1), top_p or min_p outside [0, 1]
+ * (SPEC_DEV_BAD_FILTER), a temperature not finite and > 0 (SPEC_DEV_BAD_TEMP)
+ * and a row with a NaN, +inf or only -inf (SPEC_DEV_BAD_LOGIT).
+ * Rows as in spec_logprobs; 1 <= B * n <= 2^20, 1 <= V < 2^24.               */
+typedef struct {
+  int32_t B, n, V, dtype;
+  const void* logits;
+  int64_t b_stride, row_stride;
+  const float* u;             /* [B][n]                                         */
+  const float* temperature;   /* optional [B]: 1                                */
+  const int32_t* top_k;       /* optional [B]                                   */
+  const float* top_p;         /* optional [B]                                   */
+  const float* min_p;         /* optional [B]                                   */
+  int32_t* tokens;            /* out [B][n]                                     */
+  float* logprob;             /* optional out [B][n]                            */
+  int32_t* kept;              /* optional out [B][n]                            */
+  uint32_t* dev_status;
+} spec_sample_args;
+int32_t spec_sample(const spec_sample_args* args, spec_stream_t stream);
 
 /* ---------------------------------------------- operating-point report */
 /* The analytic speed-up model of "Speculative Decoding Part 1: 도입 전에 확인해야

@@ -23,7 +23,7 @@ SPEC_OPT_DRAFT_KERNEL = 8
 SPEC_OPT_VERIFY_KERNEL = 9
 DEV_BITS = {1: "BAD_TOKEN", 2: "BAD_LEN", 4: "BAD_TEMP", 8: "TIMEOUT", 16: "REFINED",
             32: "OVERFLOW", 64: "BAD_CONF", 128: "BAD_TREE", 256: "NO_PAGES", 512: "BAD_SLOT",
-            1024: "BAD_LOGIT", 2048: "BAD_KV"}
+            1024: "BAD_LOGIT", 2048: "BAD_KV", 4096: "BAD_FILTER", 8192: "BAD_POSITION"}
 
 EXPORTED = ("spec_workspace_bytes", "spec_markov_draft", "spec_markov_draft_static",
             "spec_verify", "spec_status_string",
@@ -33,7 +33,9 @@ EXPORTED = ("spec_workspace_bytes", "spec_markov_draft", "spec_markov_draft_stat
             "spec_rnn_draft", "spec_tree_select", "spec_tree_draft", "spec_tree_verify",
             "spec_tree_workspace_bytes", "spec_cycle_host", "spec_cache_bytes",
             "spec_block_tables", "spec_cache_append", "spec_cache_attention_workspace_bytes",
-            "spec_cache_attention", "spec_logprobs_workspace_bytes", "spec_logprobs")
+            "spec_cache_attention", "spec_logprobs_workspace_bytes", "spec_logprobs",
+            "spec_rotary_append", "spec_prefix_attention_workspace_bytes", "spec_prefix_attention",
+            "spec_sample")
 
 
 class SpecError(RuntimeError):
@@ -144,6 +146,29 @@ class CacheAttentionArgs(ctypes.Structure):
                 ("workspace_bytes", _sz)]
 
 
+class PrefixAttentionArgs(ctypes.Structure):
+    _fields_ = [("own", CacheAttentionArgs), ("groups", _i32), ("prefix_stride", _i32),
+                ("prefix_table", _vp), ("prefix_len", _vp), ("group_ptr", _vp)]
+
+
+class RotaryAppendArgs(ctypes.Structure):
+    _fields_ = [("T", _i32), ("Hq", _i32), ("Hkv", _i32), ("D", _i32), ("R", _i32), ("dtype", _i32),
+                ("page_size", _i32), ("num_pages", _i32), ("rope_rows", _i32), ("interleaved", _i32),
+                ("q", _vp), ("k", _vp), ("v", _vp), ("q_row_stride", _i64), ("q_head_stride", _i64),
+                ("k_row_stride", _i64), ("k_head_stride", _i64), ("v_row_stride", _i64),
+                ("v_head_stride", _i64), ("q_weight", _vp), ("k_weight", _vp), ("positions", _vp),
+                ("slots", _vp), ("rope", _vp), ("eps", _f32), ("k_scale", _f32), ("v_scale", _f32),
+                ("q_out", _vp), ("q_out_row_stride", _i64), ("q_out_head_stride", _i64),
+                ("cache", _vp), ("k_stored", _vp), ("v_stored", _vp), ("dev_status", _vp)]
+
+
+class SampleArgs(ctypes.Structure):
+    _fields_ = [("B", _i32), ("n", _i32), ("V", _i32), ("dtype", _i32), ("logits", _vp),
+                ("b_stride", _i64), ("row_stride", _i64), ("u", _vp), ("temperature", _vp),
+                ("top_k", _vp), ("top_p", _vp), ("min_p", _vp), ("tokens", _vp), ("logprob", _vp),
+                ("kept", _vp), ("dev_status", _vp)]
+
+
 class LogprobsArgs(ctypes.Structure):
     _fields_ = [("B", _i32), ("n", _i32), ("V", _i32), ("K", _i32), ("dtype", _i32),
                 ("logits", _vp), ("b_stride", _i64), ("row_stride", _i64), ("tokens", _vp),
@@ -218,6 +243,14 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     L.spec_logprobs_workspace_bytes.argtypes = [_i32, _i32, _i32]
     L.spec_logprobs.restype = _i32
     L.spec_logprobs.argtypes = [_vp, _vp]
+    L.spec_rotary_append.restype = _i32
+    L.spec_rotary_append.argtypes = [_vp, _vp]
+    L.spec_prefix_attention_workspace_bytes.restype = _sz
+    L.spec_prefix_attention_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32]
+    L.spec_prefix_attention.restype = _i32
+    L.spec_prefix_attention.argtypes = [_vp, _vp]
+    L.spec_sample.restype = _i32
+    L.spec_sample.argtypes = [_vp, _vp]
     if path is None:
         _LIB = L
     return L
@@ -461,12 +494,18 @@ def spec_tree_verify(target, U, W1, W2, anchor, temperature, parent, mask, token
 
 def _format(py) -> struct.Struct:
     """struct format of a mirror, native alignment."""
+    return struct.Struct("@" + _codes(py) + "0P")
+
+
+def _codes(py) -> str:
     codes = {_i32: "i", _vp: "P", _i64: "q", _f32: "f", _sz: "N"}
-    return struct.Struct("@" + "".join(codes[t] for _, t in py._fields_) + "0P")
+    # a structure within it ends on a pointer's boundary
+    return "".join(codes[t] if t in codes else _codes(t) + "0P" for _, t in py._fields_)
 
 
 _TABLES, _APPEND = _format(BlockTablesArgs), _format(CacheAppendArgs)
 _ATTENTION, _LOGPROBS = _format(CacheAttentionArgs), _format(LogprobsArgs)
+_PREFIX, _ROTARY, _SAMPLE = _format(PrefixAttentionArgs), _format(RotaryAppendArgs), _format(SampleArgs)
 
 
 def _pack(fmt: struct.Struct, *values) -> bytes:
@@ -583,13 +622,10 @@ def spec_cache_attention_workspace_bytes(Hq: int, Hkv: int, D: int) -> int:
     return int(lib().spec_cache_attention_workspace_bytes(Hq, Hkv, D))
 
 
-def spec_cache_attention(q, cache, block_table, kv_len, row_ptr, out, dev_status, workspace,
-                         softmax_scale: float, k_scale: float = 1.0, v_scale: float = 1.0,
-                         tree_mask=None, lse=None, stream=None) -> None:
-    """Attention of the packed rows q [T][Hq][D] of every request over its
-    cached tokens; tree_mask [T][words] (int32 bit words) replaces the causal
-    order among a request's new tokens."""
-    T = _types()
+def _attention_values(dev, q, cache, block_table, kv_len, row_ptr, out, dev_status, workspace,
+                      softmax_scale, k_scale, v_scale, tree_mask, lse) -> tuple:
+    """The fields of spec_cache_attention_args."""
+    T = _torch
     i32 = T.int32
     shape, table = tuple(q.shape), tuple(block_table.shape)
     if len(shape) != 3 or len(table) != 2:
@@ -600,17 +636,106 @@ def spec_cache_attention(q, cache, block_table, kv_len, row_ptr, out, dev_status
     if tree_mask is not None and tree_mask.dim() != 2:
         raise SpecError(f"tree_mask must be [T, words], not {list(tree_mask.shape)}")
     words = 0 if tree_mask is None else tree_mask.shape[1]
-    dev = _device()
     qp, qr, qh, cp, tp, lp, rp, mp, op, ep, st, wp, wn = _args.addresses(
         dev, "q", q, None, shape, "cache", cache, T.uint8, (pages, Hkv, P // 16, 18 * D),
         "block_table", block_table, i32, table, "kv_len", kv_len, i32, (B,), "row_ptr", row_ptr, i32, (B + 1,),
         "tree_mask?", tree_mask, i32, (rows, words), "out", out, q.dtype, shape, "lse?", lse, T.float32, (rows, Hq),
         "dev_status", dev_status, i32, (4,), "workspace", workspace, None, None)
-    a = _pack(_ATTENTION, B, rows, Hq, Hkv, D, _storage(q), P, pages, table[1], words, qp, qr, qh, cp, tp, lp,
-              rp, mp, softmax_scale, k_scale, v_scale, op, ep, st, wp, wn)
+    return (B, rows, Hq, Hkv, D, _storage(q), P, pages, table[1], words, qp, qr, qh, cp, tp, lp, rp, mp,
+            softmax_scale, k_scale, v_scale, op, ep, st, wp, wn)
+
+
+def spec_cache_attention(q, cache, block_table, kv_len, row_ptr, out, dev_status, workspace,
+                         softmax_scale: float, k_scale: float = 1.0, v_scale: float = 1.0,
+                         tree_mask=None, lse=None, stream=None) -> None:
+    """Attention of the packed rows q [T][Hq][D] of every request over its
+    cached tokens; tree_mask [T][words] (int32 bit words) replaces the causal
+    order among a request's new tokens."""
+    _types()
+    dev = _device()
+    a = _pack(_ATTENTION, *_attention_values(dev, q, cache, block_table, kv_len, row_ptr, out, dev_status, workspace,
+                                             softmax_scale, k_scale, v_scale, tree_mask, lse))
     rc = lib().spec_cache_attention(a, _raw_stream(dev, stream))
     if rc:
         _check(rc, "spec_cache_attention")
+
+
+def spec_prefix_attention_workspace_bytes(T: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(lib().spec_prefix_attention_workspace_bytes(T, Hq, Hkv, D))
+
+
+def spec_prefix_attention(q, cache, block_table, kv_len, row_ptr, prefix_table, prefix_len, group_ptr, out,
+                          dev_status, workspace, softmax_scale: float, k_scale: float = 1.0,
+                          v_scale: float = 1.0, tree_mask=None, lse=None, stream=None) -> None:
+    """spec_cache_attention with prefixes that groups of requests share: requests
+    group_ptr[g] .. group_ptr[g + 1] - 1 see the first prefix_len[g] tokens of
+    prefix_table[g] before their own, which block_table and kv_len describe."""
+    T = _types()
+    dev = _device()
+    own = _attention_values(dev, q, cache, block_table, kv_len, row_ptr, out, dev_status, workspace,
+                            softmax_scale, k_scale, v_scale, tree_mask, lse)
+    table = tuple(prefix_table.shape)
+    if len(table) != 2:
+        raise SpecError(f"prefix_table must be [groups, pages], not {list(table)}")
+    a = _pack(_PREFIX, *own, *table, *_args.addresses(
+        dev, "prefix_table", prefix_table, T.int32, table, "prefix_len", prefix_len, T.int32, (table[0],),
+        "group_ptr", group_ptr, T.int32, (table[0] + 1,)))
+    rc = lib().spec_prefix_attention(a, _raw_stream(dev, stream))
+    if rc:
+        _check(rc, "spec_prefix_attention")
+
+
+def spec_rotary_append(q, k, v, positions, slots, rope, q_out, cache, dev_status, k_scale: float = 1.0,
+                       v_scale: float = 1.0, q_weight=None, k_weight=None, eps: float = 1e-6,
+                       interleaved: bool = False, k_stored=None, v_stored=None, stream=None) -> None:
+    """Norm queries and keys per head (with a weight), rotate them by rope
+    [rows][R / 2][2] (cosine, sine) at each row's position, write the queries to
+    q_out and the keys and values into the cache at their slots."""
+    T = _types()
+    qs, shape, rs = tuple(q.shape), tuple(k.shape), tuple(rope.shape)
+    if len(qs) != 3 or len(shape) != 3 or len(rs) != 3 or rs[2] != 2:
+        raise SpecError(f"q must be [T, Hq, D], k [T, Hkv, D] and rope [rows, R / 2, 2], not {list(qs)}, "
+                        f"{list(shape)}, {list(rs)}")
+    rows, H, D = shape
+    pages, Hkv, P = _cache_shape(cache, D)
+    dt = q.dtype
+    if qs[0] != rows or qs[2] != D or Hkv != H or k.dtype is not dt or v.dtype is not dt or q_out.dtype is not dt:
+        raise SpecError(f"q, k, v, q_out and cache disagree: q {list(qs)} {dt}, k {list(shape)} {k.dtype}, "
+                        f"v {v.dtype}, q_out {q_out.dtype}, cache of {Hkv} heads")
+    i32 = T.int32
+    dev = _device()
+    qp, qr, qh, kp, kr, kh, vp, vr, vh, wq, wk, pp, sp, rp, op, orow, ohead, cp, ks, vs, st = _args.addresses(
+        dev, "q", q, None, qs, "k", k, None, shape, "v", v, None, shape, "q_weight?", q_weight, dt, (D,),
+        "k_weight?", k_weight, dt, (D,), "positions", positions, i32, (rows,), "slots", slots, i32, (rows,),
+        "rope", rope, T.float32, rs, "q_out", q_out, None, qs, "cache", cache, T.uint8, (pages, H, P // 16, 18 * D),
+        "k_stored?", k_stored, dt, shape, "v_stored?", v_stored, dt, shape, "dev_status", dev_status, i32, (4,))
+    a = _pack(_ROTARY, rows, qs[1], H, D, 2 * rs[1], _storage(q), P, pages, rs[0], 1 if interleaved else 0, qp, kp, vp,
+              qr, qh, kr, kh, vr, vh, wq, wk, pp, sp, rp, eps, k_scale, v_scale, op, orow, ohead, cp, ks, vs, st)
+    rc = lib().spec_rotary_append(a, _raw_stream(dev, stream))
+    if rc:
+        _check(rc, "spec_rotary_append")
+
+
+def spec_sample(logits, u, tokens, dev_status, temperature=None, top_k=None, top_p=None, min_p=None,
+                logprob=None, kept=None, stream=None) -> None:
+    """Draw a token of each row of logits [B][n][V] with the uniform numbers u
+    [B][n], after temperature, top_k, top_p and min_p ([B] each)."""
+    T = _types()
+    f32, i32 = T.float32, T.int32
+    shape = tuple(logits.shape)
+    if len(shape) != 3:
+        raise SpecError(f"logits must be [B, n, V], not {list(shape)}")
+    B, n, V = shape
+    b, bn = (B,), (B, n)
+    dev = _device()
+    xp, xb, xr, *rest = _args.addresses(
+        dev, "logits", logits, None, shape, "u", u, f32, bn, "temperature?", temperature, f32, b,
+        "top_k?", top_k, i32, b, "top_p?", top_p, f32, b, "min_p?", min_p, f32, b, "tokens", tokens, i32, bn,
+        "logprob?", logprob, f32, bn, "kept?", kept, i32, bn, "dev_status", dev_status, i32, (4,))
+    a = _pack(_SAMPLE, B, n, V, _storage(logits), xp, xb, xr, *rest)
+    rc = lib().spec_sample(a, _raw_stream(dev, stream))
+    if rc:
+        _check(rc, "spec_sample")
 
 
 def spec_logprobs_workspace_bytes(rows: int, V: int, K: int) -> int:

@@ -69,6 +69,10 @@ cudaError_t launch_cache_append(const spec_cache_append_args&, cudaStream_t);
 size_t cache_attention_workspace_bytes(int, int, int);
 float cache_attention_scale(const spec_cache_attention_args&);
 cudaError_t launch_cache_attention(const spec_cache_attention_args&, int, cudaStream_t);
+cudaError_t launch_rotary_append(const spec_rotary_append_args&, int, cudaStream_t);
+size_t prefix_attention_workspace_bytes(int, int, int, int);
+cudaError_t launch_prefix_attention(const spec_prefix_attention_args&, int, cudaStream_t);
+cudaError_t launch_sample(const spec_sample_args&, int, cudaStream_t);
 size_t logprobs_workspace_bytes(int, int, int);
 cudaError_t launch_logprobs(const spec_logprobs_args&, cudaStream_t);
 
@@ -114,13 +118,15 @@ enum Stage {
   ST_DRAFT_PERSISTENT, ST_DRAFT_SLICE, ST_VERIFY_PREP,
   ST_TARGET_STATS, ST_VERIFY_TILE, ST_VERIFY_SLICE, ST_VERIFY_FINAL, ST_SLOW_VERIFY, ST_VERIFY_HP_SUMS,
   ST_VERIFY_HP_RESID, ST_VERIFY_REDECIDE, ST_CONFIDENCE, ST_SCHED_RANK, ST_SCHED_SELECT, ST_TREE_SELECT,
-  ST_TREE_DRAFT, ST_TREE_VERIFY, ST_BLOCK_TABLES, ST_CACHE_APPEND, ST_CACHE_ATTENTION, ST_LOGPROBS, ST_COUNT
+  ST_TREE_DRAFT, ST_TREE_VERIFY, ST_BLOCK_TABLES, ST_CACHE_APPEND, ST_CACHE_ATTENTION, ST_LOGPROBS, ST_ROTARY_APPEND,
+  ST_PREFIX_ATTENTION, ST_SAMPLE, ST_COUNT
 };
 const char* kStageNames[ST_COUNT] = {
     "draft_persistent", "draft_slice", "verify_prep",
     "target_stats", "verify_tile", "verify_slice", "verify_final", "slow_verify", "verify_hp_sums",
     "verify_hp_resid", "verify_redecide", "confidence", "sched_rank", "sched_select", "tree_select",
-    "tree_draft", "tree_verify", "block_tables", "cache_append", "cache_attention", "logprobs"};
+    "tree_draft", "tree_verify", "block_tables", "cache_append", "cache_attention", "logprobs", "rotary_append",
+    "prefix_attention", "sample"};
 bool g_prof = false;
 struct EvPair { cudaEvent_t a, b; int stage; };
 std::vector<EvPair> g_pending;
@@ -825,8 +831,8 @@ size_t spec_cache_attention_workspace_bytes(int32_t Hq, int32_t Hkv, int32_t D) 
   return cache_attention_workspace_bytes(Hq, Hkv, D);
 }
 
-int32_t spec_cache_attention(const spec_cache_attention_args* a, spec_stream_t stream) {
-  if (!a) return SPEC_EINVAL;
+// What spec_cache_attention asks of its arguments, the workspace aside; 1: no rows.
+static int32_t attention_check(const spec_cache_attention_args* a) {
   if (a->B < 1 || a->B > 4096 || a->T < 0 || a->T >= (1 << 24) || a->Hkv < 1 || a->Hq < a->Hkv ||
       a->Hq > 256 || a->Hq % a->Hkv != 0 || (int64_t)a->T * a->Hq > 0x7fffffff - 255 ||   // rows in whole tiles
       a->num_pages < 1 || a->table_stride < 1 ||
@@ -836,13 +842,20 @@ int32_t spec_cache_attention(const spec_cache_attention_args* a, spec_stream_t s
     return SPEC_EINVAL;
   if (!page_ok(a->page_size) || !head_ok(a->D) || (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16))
     return SPEC_EUNSUPPORTED;
-  if (a->T == 0) return SPEC_OK;
+  if (a->T == 0) return 1;
   if (!a->q || !a->cache || !a->block_table || !a->kv_len || !a->row_ptr || !a->out || !a->dev_status)
     return SPEC_EINVAL;
   if (!aligned(a->q, 16) || !aligned(a->cache, 16) || !aligned(a->block_table, 4) || !aligned(a->kv_len, 4) ||
       !aligned(a->row_ptr, 4) || !aligned(a->tree_mask, 4) || !aligned(a->out, 16) || !aligned(a->lse, 4) ||
       !aligned(a->dev_status, 4) || !stride_ok(a->q_row_stride, a->dtype) || !stride_ok(a->q_head_stride, a->dtype))
     return SPEC_EALIGN;
+  return SPEC_OK;
+}
+
+int32_t spec_cache_attention(const spec_cache_attention_args* a, spec_stream_t stream) {
+  if (!a) return SPEC_EINVAL;
+  const int32_t rc = attention_check(a);
+  if (rc != SPEC_OK) return rc > 0 ? SPEC_OK : rc;
   if (!a->workspace || a->workspace_bytes < spec_cache_attention_workspace_bytes(a->Hq, a->Hkv, a->D))
     return SPEC_EWORKSPACE;
   if (!aligned(a->workspace, 16)) return SPEC_EALIGN;
@@ -851,6 +864,78 @@ int32_t spec_cache_attention(const spec_cache_attention_args* a, spec_stream_t s
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope p(st, ST_CACHE_ATTENTION);
   return launch_cache_attention(*a, sms, st) == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}
+
+size_t spec_prefix_attention_workspace_bytes(int32_t T, int32_t Hq, int32_t Hkv, int32_t D) {
+  const size_t base = spec_cache_attention_workspace_bytes(Hq, Hkv, D);
+  if (base == 0 || T < 0 || T >= (1 << 24) || (int64_t)T * Hq > 0x7fffffff - 255) return 0;
+  return prefix_attention_workspace_bytes(T, Hq, Hkv, D);
+}
+
+int32_t spec_prefix_attention(const spec_prefix_attention_args* a, spec_stream_t stream) {
+  if (!a) return SPEC_EINVAL;
+  const spec_cache_attention_args* o = &a->own;
+  if (a->groups < 1 || a->groups > 4096 || a->prefix_stride < 1 || (int64_t)a->groups * a->prefix_stride > 0x7fffffff)
+    return SPEC_EINVAL;
+  const int32_t rc = attention_check(o);
+  if (rc != SPEC_OK) return rc > 0 ? SPEC_OK : rc;
+  if (!a->prefix_table || !a->prefix_len || !a->group_ptr) return SPEC_EINVAL;
+  if (!aligned(a->prefix_table, 4) || !aligned(a->prefix_len, 4) || !aligned(a->group_ptr, 4)) return SPEC_EALIGN;
+  if (!o->workspace || o->workspace_bytes < spec_prefix_attention_workspace_bytes(o->T, o->Hq, o->Hkv, o->D))
+    return SPEC_EWORKSPACE;
+  if (!aligned(o->workspace, 16)) return SPEC_EALIGN;
+  const int sms = num_sms();
+  if (sms <= 0) return SPEC_ECUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope p(st, ST_PREFIX_ATTENTION);
+  return launch_prefix_attention(*a, sms, st) == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}
+
+int32_t spec_rotary_append(const spec_rotary_append_args* a, spec_stream_t stream) {
+  if (!a) return SPEC_EINVAL;
+  if (a->T < 0 || a->T >= (1 << 24) || a->Hq < 1 || a->Hq > 256 || a->Hkv < 1 || a->Hkv > 256 || a->num_pages < 1 ||
+      (int64_t)a->num_pages * a->page_size > 0x7fffffff || a->rope_rows < 1 || !cache_scale_ok(a->k_scale) ||
+      !cache_scale_ok(a->v_scale) || !(a->eps >= 0.f && a->eps <= 3.402823466e38f))
+    return SPEC_EINVAL;
+  if (!page_ok(a->page_size) || !head_ok(a->D) || (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) || a->R < 32 ||
+      a->R > a->D || a->R % 32 != 0)
+    return SPEC_EUNSUPPORTED;
+  if (((int64_t)a->T + 16) * (a->Hq > a->Hkv ? a->Hq : a->Hkv) * a->D >= (int64_t)1 << 36) return SPEC_EINVAL;
+  if (a->T == 0) return SPEC_OK;
+  if (!a->q || !a->k || !a->v || !a->positions || !a->slots || !a->rope || !a->q_out || !a->cache || !a->dev_status)
+    return SPEC_EINVAL;
+  if (!aligned(a->q, 16) || !aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(a->q_weight, 16) ||
+      !aligned(a->k_weight, 16) || !aligned(a->positions, 4) || !aligned(a->slots, 4) || !aligned(a->rope, 16) ||
+      !aligned(a->q_out, 16) || !aligned(a->cache, 16) || !aligned(a->k_stored, 16) || !aligned(a->v_stored, 16) ||
+      !aligned(a->dev_status, 4))
+    return SPEC_EALIGN;
+  for (int64_t s : {a->q_row_stride, a->q_head_stride, a->k_row_stride, a->k_head_stride, a->v_row_stride,
+                    a->v_head_stride, a->q_out_row_stride, a->q_out_head_stride})
+    if (!stride_ok(s, a->dtype)) return SPEC_EALIGN;
+  // in place, every element is written by the thread that read it; otherwise not at all
+  if (a->q_out == a->q && (a->q_out_row_stride != a->q_row_stride || a->q_out_head_stride != a->q_head_stride))
+    return SPEC_EINVAL;
+  const int sms = num_sms();
+  if (sms <= 0) return SPEC_ECUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope p(st, ST_ROTARY_APPEND);
+  return launch_rotary_append(*a, sms, st) == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}
+
+int32_t spec_sample(const spec_sample_args* a, spec_stream_t stream) {
+  if (!a) return SPEC_EINVAL;
+  if (a->B < 1 || a->n < 1 || (int64_t)a->B * a->n > (1 << 20) || a->V < 1 || a->V >= (1 << 24)) return SPEC_EINVAL;
+  if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_EUNSUPPORTED;
+  if (!a->logits || !a->u || !a->tokens || !a->dev_status) return SPEC_EINVAL;
+  if (!aligned(a->logits, 16) || !aligned(a->u, 4) || !aligned(a->temperature, 4) || !aligned(a->top_k, 4) ||
+      !aligned(a->top_p, 4) || !aligned(a->min_p, 4) || !aligned(a->tokens, 4) || !aligned(a->logprob, 4) ||
+      !aligned(a->kept, 4) || !aligned(a->dev_status, 4))
+    return SPEC_EALIGN;
+  const int sms = num_sms();
+  if (sms <= 0) return SPEC_ECUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope p(st, ST_SAMPLE);
+  return launch_sample(*a, sms, st) == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }
 
 size_t spec_logprobs_workspace_bytes(int32_t rows, int32_t V, int32_t K) {

@@ -226,7 +226,7 @@ struct RowTiles {
       mref[i] = -INFINITY;
       l[i] = 0.f;
       const int r = sg.tile * ROWS + 16 * (i >> 1) + 8 * (i & 1) + g;
-      lim[i] = r < rows ? (p.mask ? sg.r0 + r / p.G : sg.L - sg.n + r / p.G + 1) : -1;
+      lim[i] = r < rows ? (p.cut ? sg.L : p.mask ? sg.r0 + r / p.G : sg.L - sg.n + r / p.G + 1) : -1;
     }
 #pragma unroll
     for (int m = 0; m < M; ++m)
@@ -264,7 +264,7 @@ struct RowTiles {
       }
     }
     // ---- masks, where the unit reaches the new tokens
-    const int tok0 = u * AT_UNIT, ctx = sg.L - sg.n;
+    const int tok0 = u * AT_UNIT, ctx = sg.context(p);
     if (tok0 + AT_UNIT > ctx) {
       clear_unwritten<C>(unit, tok0, sg.L, lane);
 #pragma unroll
@@ -426,7 +426,7 @@ struct ColumnTile {
       mref[i] = -INFINITY;
       l[i] = 0.f;
       const int r = sg.tile * ROWS + 2 * t + i;
-      lim[i] = r < rows ? (p.mask ? sg.r0 + r / p.G : sg.L - sg.n + r / p.G + 1) : -1;
+      lim[i] = r < rows ? (p.cut ? sg.L : p.mask ? sg.r0 + r / p.G : sg.L - sg.n + r / p.G + 1) : -1;
     }
 #pragma unroll
     for (int j = 0; j < NV / 2; ++j)
@@ -462,7 +462,7 @@ struct ColumnTile {
       }
     }
     // ---- masks, where the unit reaches the new tokens
-    const int tok0 = u * AT_UNIT, ctx = sg.L - sg.n;
+    const int tok0 = u * AT_UNIT, ctx = sg.context(p);
     if (tok0 + AT_UNIT > ctx) {
       clear_unwritten<C>(unit, tok0, sg.L, lane);
 #pragma unroll
@@ -719,17 +719,28 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
         const float m = tile.mref[i] == -INFINITY ? -INFINITY : tile.c[i] * tile.mref[i] - AT_SHIFT;
         if (whole) {
           const int tok = r / p.G, hq = sg.h * p.G + r - tok * p.G;
-          const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
           const size_t at = (size_t)(sg.r0 + tok) * p.Hq + hq;
+          if (p.raw) {
+#pragma unroll
+            for (int q = 0; q < C::QUADS; ++q) {
+              float x[4];
+              tile.quad(i, q, x);
+              store4(p.raw + at * C::D + C::column(q, lane), x);
+            }
+            if (C::first(lane)) p.raw_ml[at] = make_float2(m, sum);
+            continue;
+          }
+          const AttnRow f = attn_row(p, at, m, sum);
 #pragma unroll
           for (int q = 0; q < C::QUADS; ++q) {
             float x[4];
             tile.quad(i, q, x);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) x[v] *= inv;
+            for (int v = 0; v < 4; ++v) x[v] *= f.own;
+            if (p.prefix) add_prefix4(p.prefix + at * C::D + C::column(q, lane), f.prefix, x);
             store4(static_cast<DT*>(p.out) + at * C::D + C::column(q, lane), x);
           }
-          if (C::first(lane) && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : 0.69314718056f * (m + log2f(sum));
+          if (C::first(lane) && p.lse) p.lse[at] = f.lse;
         } else {
 #pragma unroll
           for (int q = 0; q < C::QUADS; ++q) {
@@ -801,11 +812,14 @@ float cache_attention_scale(const spec_cache_attention_args& a) {
   return a.softmax_scale * a.k_scale * 1.4426950408889634f;
 }
 
-cudaError_t launch_cache_attention(const spec_cache_attention_args& a, int sms, cudaStream_t st) {
-  const int G = a.Hq / a.Hkv;
-  AttnParams p{a.B, a.T, a.Hq, a.Hkv, G, a.page_size, a.num_pages, a.table_stride, a.mask_words, a.q, a.q_row_stride,
-               a.q_head_stride, a.cache, a.block_table, a.kv_len, a.row_ptr, a.tree_mask,
-               cache_attention_scale(a), a.v_scale, a.out, a.lse, a.dev_status, a.workspace};
+namespace {
+AttnParams own_params(const spec_cache_attention_args& a) {
+  return AttnParams{a.B, a.T, a.Hq, a.Hkv, a.Hq / a.Hkv, a.page_size, a.num_pages, a.table_stride, a.mask_words, a.q,
+                    a.q_row_stride, a.q_head_stride, a.cache, a.block_table, a.kv_len, a.row_ptr, a.tree_mask,
+                    cache_attention_scale(a), a.v_scale, a.out, a.lse, a.dev_status, a.workspace};
+}
+
+cudaError_t launch_tiles(const AttnParams& p, int D, int dtype, int sms, cudaStream_t st) {
   // The tile by the mean rows a request (finished requests and rows of no request
   // count in it: the host does not see them).  Times are us a call of these
   // kernels, cold caches, D = 128, 4 query heads a key-value head, all requests of
@@ -819,11 +833,11 @@ cudaError_t launch_cache_attention(const spec_cache_attention_args& a, int sms, 
   //     requests of 20 rows would gain too (280 against 328, 166 against 191), but
   //     blocks of mixed sizes hardly do (b, 8 to 32 rows: 256 against 268) or lose
   //     (c, 8 to 20 rows: 165 against 131).
-  const long long rows = (long long)a.T * G;
-  const bool few = rows <= 8LL * a.B, wide = rows > 24LL * a.B && rows <= 32LL * a.B;
-  if (a.dtype == SPEC_F32) {
-    if (a.D == 64) return few ? launch_cfg<ColumnTile<64, 2>, float>(p, sms, st) : launch_cfg<RowTiles<64, 1, 2>, float>(p, sms, st);
-    if (a.D == 128)
+  const long long rows = (long long)p.T * p.G;
+  const bool few = rows <= 8LL * p.B, wide = rows > 24LL * p.B && rows <= 32LL * p.B;
+  if (dtype == SPEC_F32) {
+    if (D == 64) return few ? launch_cfg<ColumnTile<64, 2>, float>(p, sms, st) : launch_cfg<RowTiles<64, 1, 2>, float>(p, sms, st);
+    if (D == 128)
       return few ? launch_cfg<ColumnTile<128, 2>, float>(p, sms, st) : launch_cfg<RowTiles<128, 1, 2>, float>(p, sms, st);
     return few ? launch_cfg<ColumnTile<256, 2>, float>(p, sms, st) : launch_cfg<RowTiles<256, 1, 2>, float>(p, sms, st);
   }
@@ -831,16 +845,49 @@ cudaError_t launch_cache_attention(const spec_cache_attention_args& a, int sms, 
   //     492, 274 in 16-row tiles and 122, 533, 286 in 32-row tiles; 100 rows 75,
   //     379, 235 against 211, 1120, 596.  At 32 rows (b) 347, (c) 219 lose to 305
   //     and 170, and only (a) would gain (64 against 83).
-  if (a.D <= 128 && rows > 32LL * a.B) return launch_cache_attention_tc(p, a.D, sms, st);
-  if (a.D == 64)
+  if (D <= 128 && rows > 32LL * p.B) return launch_cache_attention_tc(p, D, sms, st);
+  if (D == 64)
     return few    ? launch_cfg<ColumnTile<64, 1>, bf16>(p, sms, st)
            : wide ? launch_cfg<RowTiles<64, 2, 1>, bf16>(p, sms, st)
                   : launch_cfg<RowTiles<64, 1, 1>, bf16>(p, sms, st);
-  if (a.D == 128)
+  if (D == 128)
     return few    ? launch_cfg<ColumnTile<128, 1>, bf16>(p, sms, st)
            : wide ? launch_cfg<RowTiles<128, 2, 1>, bf16>(p, sms, st)
                   : launch_cfg<RowTiles<128, 1, 1>, bf16>(p, sms, st);
   return few ? launch_cfg<ColumnTile<256, 1>, bf16>(p, sms, st) : launch_cfg<RowTiles<256, 1, 1>, bf16>(p, sms, st);
+}
+}  // namespace
+
+cudaError_t launch_cache_attention(const spec_cache_attention_args& a, int sms, cudaStream_t st) {
+  return launch_tiles(own_params(a), a.D, a.dtype, sms, st);
+}
+
+// Attention with shared prefixes: the groups' rows over their prefixes, then every
+// request's over its own tokens, whose end adds the two.  Workspace: that of a pass,
+// a word, the prefixes' sums.
+size_t prefix_attention_workspace_bytes(int T, int Hq, int Hkv, int D) {
+  return cache_attention_workspace_bytes(Hq, Hkv, D) + 256 + (size_t)T * Hq * (D * sizeof(float) + sizeof(float2));
+}
+
+cudaError_t launch_prefix_attention(const spec_prefix_attention_args& a, int sms, cudaStream_t st) {
+  const spec_cache_attention_args& o = a.own;
+  AttnParams own = own_params(o), shared = own;
+  char* ws = static_cast<char*>(o.workspace) + (cache_attention_workspace_bytes(o.Hq, o.Hkv, o.D) + 15) / 16 * 16;
+  shared.B = a.groups;
+  shared.stride = a.prefix_stride;
+  shared.table = a.prefix_table;
+  shared.kv_len = a.prefix_len;
+  shared.mask = nullptr;
+  shared.cut = a.group_ptr;
+  shared.members = o.B;
+  shared.ranges = reinterpret_cast<int*>(ws);
+  shared.raw = reinterpret_cast<float*>(ws + 128);
+  shared.raw_ml = reinterpret_cast<float2*>(shared.raw + (size_t)o.T * o.Hq * o.D);
+  own.prefix = shared.raw;
+  own.prefix_ml = shared.raw_ml;
+  own.prefix_ranges = shared.ranges;
+  const cudaError_t e = launch_tiles(shared, o.D, o.dtype, sms, st);
+  return e != cudaSuccess ? e : launch_tiles(own, o.D, o.dtype, sms, st);
 }
 
 }  // namespace spec

@@ -23,6 +23,17 @@ struct AttnParams {
   float* lse;
   uint32_t* status;
   void* ws;
+  // The pass over shared prefixes: "requests" are groups of requests, whose rows see
+  // every token, and sums are left unnormalised for the pass over own tokens.
+  const int* cut;                         // [B+1] first request of each group (null: not that pass)
+  int members;                            // requests of all groups
+  float* raw;                             // [T][Hq][D] sums, and (maximum, sum of p) a row
+  float2* raw_ml;
+  int* ranges;                            // 1 where cut and row_ptr cover every row once, else 0
+  // The pass over own tokens, after it: what to add to each row's sums.
+  const float* prefix;                    // null: nothing
+  const float2* prefix_ml;
+  const int* prefix_ranges;
 };
 
 constexpr int AT_WARPS = 8;               // workspace slots: AT_MAX_CTAS * AT_WARPS workers at most
@@ -48,6 +59,7 @@ struct AttnSeg {
   int b, h, tile, u, nu;                  // units u .. nu - 1 are left
   int n, r0, L;
   bool bad;
+  __device__ __forceinline__ int context(const AttnParams& p) const { return p.cut ? L : L - n; }   // tokens before the new ones
 };
 
 // Units of request b over all heads and row tiles (0: nothing to do).  LEAD: what
@@ -55,20 +67,28 @@ struct AttnSeg {
 template <int ROWS, int UNIT, int LEAD>
 __device__ __forceinline__ long long attn_work(const AttnParams& p, int b, int& n, int& r0, int& L, int& tiles,
                                                int& nu, bool& bad, bool& outside) {
-  r0 = __ldg(p.row_ptr + b);
-  const int r1 = __ldg(p.row_ptr + b + 1);
+  int b0 = b, b1 = b + 1;
+  outside = false;
+  if (p.cut) {
+    b0 = __ldg(p.cut + b);
+    b1 = __ldg(p.cut + b + 1);
+    outside = b0 < 0 || b1 < b0 || b1 > p.members;
+    if (outside) b0 = b1 = 0;
+  }
+  r0 = __ldg(p.row_ptr + b0);
+  const int r1 = __ldg(p.row_ptr + b1);
   L = __ldg(p.kv_len + b);
   n = r1 - r0;
-  outside = r0 < 0 || r1 < r0 || r1 > p.T;
+  outside |= r0 < 0 || r1 < r0 || r1 > p.T;
   bad = false;
   if (outside || n == 0) {
     n = 0;
     tiles = nu = 0;
     return 0;
   }
-  bad = L < n || L > (1 << 30) || L > (long long)p.stride * p.P;
+  bad = L < (p.cut ? 0 : n) || L > (1 << 30) || L > (long long)p.stride * p.P;
   tiles = (n * p.G + ROWS - 1) / ROWS;
-  nu = bad ? 1 : (L + UNIT - 1) / UNIT;
+  nu = bad || L == 0 ? 1 : (L + UNIT - 1) / UNIT;          // no prefix: one unit of which nothing is seen
   return (long long)p.Hkv * tiles * (nu + LEAD);
 }
 
@@ -106,7 +126,44 @@ __device__ __forceinline__ long long attn_prefix(const AttnParams& p, long long*
   s_pre[tid] = before + v - mine;
   if (tid == 0) s_pre[THREADS] = all;
   if (flag && blockIdx.x == 0) set_status(p.status, SPEC_DEV_BAD_LEN);
+  if (p.ranges && blockIdx.x == 0) {                       // do the groups cover every request's rows once
+    bool ok = true;
+    for (int b = tid; b <= p.members; b += THREADS) {
+      const int r = __ldg(p.row_ptr + b);
+      ok &= r >= (b > 0 ? __ldg(p.row_ptr + b - 1) : 0) && r <= p.T;
+    }
+    for (int g = tid; g <= p.B; g += THREADS) {
+      const int c = __ldg(p.cut + g);
+      ok &= c >= (g > 0 ? __ldg(p.cut + g - 1) : 0) && (g > 0 || c == 0) && (g < p.B || c == p.members);
+    }
+    sync();                                                // s_scan has been read
+    if (lane == 0) s_scan[warp] = 1;
+    __syncwarp();
+    if (!ok) s_scan[warp] = 0;
+    sync();
+    if (tid == 0) {
+      bool every = true;
+      for (int w = 0; w < THREADS / 32; ++w) every &= s_scan[w] != 0;
+      *p.ranges = every;
+      if (!every) set_status(p.status, SPEC_DEV_BAD_LEN);
+    }
+  }
   return all;
+}
+
+// What a row's sums are multiplied by at its end, and those of its prefix; lse.
+struct AttnRow {
+  float own, prefix, lse;
+};
+__device__ __forceinline__ AttnRow attn_row(const AttnParams& p, size_t at, float m, float sum) {
+  if (!p.prefix) return {sum == 0.f ? 0.f : p.v_scale / sum, 0.f, sum == 0.f ? -INFINITY : 0.69314718056f * (m + log2f(sum))};
+  const float2 v = __ldcg(p.prefix_ml + at);
+  const float top = fmaxf(m, v.x), ref = top == -INFINITY ? 0.f : top;
+  const float fa = exp2f(m - ref), fb = exp2f(v.x - ref);
+  float z = sum * fa + v.y * fb;
+  if (!__ldcg(p.prefix_ranges)) z = quiet_nan();
+  const float inv = z == 0.f ? 0.f : p.v_scale / z;
+  return {fa * inv, fb * inv, z == 0.f ? -INFINITY : 0.69314718056f * (ref + log2f(z))};
 }
 
 // The segment that holds unit `pos` (below the total); LEAD more units to `u`.
@@ -235,6 +292,15 @@ __device__ __forceinline__ void store4(float* p, const float* x) {
   *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
 }
 
+// x + f times four elements of a prefix's sums.
+__device__ __forceinline__ void add_prefix4(const float* from, float f, float (&x)[4]) {
+  const float4 v = __ldcg(reinterpret_cast<const float4*>(from));
+  x[0] = fmaf(f, v.x, x[0]);
+  x[1] = fmaf(f, v.y, x[1]);
+  x[2] = fmaf(f, v.z, x[2]);
+  x[3] = fmaf(f, v.w, x[3]);
+}
+
 // First head element of lane part t in inner step s of the first product.
 template <int D>
 __device__ __forceinline__ int k_order(int t, int s) {
@@ -346,10 +412,16 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_attention_join_kernel(cons
       const int r = s.tile * ROWS + rl;
       const int tok = r / p.G, hq = s.h * p.G + r - tok * p.G;
       const size_t at = (size_t)(s.r0 + tok) * p.Hq + hq;
-      const float inv = ml.y == 0.f ? 0.f : p.v_scale / ml.y;
-      const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+      if (p.raw) {
+        *reinterpret_cast<float4*>(p.raw + at * D + d) = acc;
+        if (d == 0) p.raw_ml[at] = ml;
+        continue;
+      }
+      const AttnRow f = attn_row(p, at, ml.x, ml.y);
+      float x[4] = {acc.x * f.own, acc.y * f.own, acc.z * f.own, acc.w * f.own};
+      if (p.prefix) add_prefix4(p.prefix + at * D + d, f.prefix, x);
       store4(static_cast<DT*>(p.out) + at * D + d, x);
-      if (d == 0 && p.lse) p.lse[at] = ml.y == 0.f ? -INFINITY : 0.69314718056f * (ml.x + log2f(ml.y));
+      if (d == 0 && p.lse) p.lse[at] = f.lse;
     }
   }
 }

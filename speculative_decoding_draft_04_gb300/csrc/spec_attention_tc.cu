@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
       const AttnSeg sg = walk.sg;
       const int u_first = sg.u, u_end = walk.u_end;
       const long long last = walk.pos + TA_LEAD + sg.nu - 1;   // the segment's last unit
-      const int ctx = sg.L - sg.n;
+      const int ctx = sg.context(p);
       const bool live = ntok >= 0;
       const int tok = live ? ntok : 0, hq = nhq;
       // ---- this thread's query as 16-bit floats, scaled by a power of two so that
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
       fence_async_shared();
       arrive(bar + TB_Q);
       bool poison = sg.bad;                                  // a page outside the cache in this part
-      const int lim = live ? (p.mask ? sg.r0 + tok : ctx + tok + 1) : -1;   // tokens it sees (causal), its packed row
+      const int lim = live ? (p.cut ? sg.L : p.mask ? sg.r0 + tok : ctx + tok + 1) : -1;   // tokens it sees (causal), its packed row
       const bool some = __any_sync(0xffffffffu, live);
       float mref = -INFINITY, l = 0.f;
       for (int u = u_first; u < u_end; ++u, ++i) {
@@ -408,20 +408,32 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
       const float m = mref == -INFINITY ? -INFINITY : c * mref - AT_SHIFT;
       float* part = attn_parts(p) + (size_t)(2 * me + slot) * L::PART;
       if (some) {
-        const float inv = l == 0.f ? 0.f : p.v_scale / l;
-        const bool sector = ((whole ? (uintptr_t)p.out : (uintptr_t)part) & 31) == 0;
         const size_t at = (size_t)(sg.r0 + tok) * p.Hq + hq;
+        AttnRow f{};
+        if (live && whole && !p.raw) f = attn_row(p, at, m, l);
+        float* const sums = !whole ? part + rl * D : p.raw + at * D;   // where they are kept as they are
+        const bool sector = ((whole && !p.raw ? (uintptr_t)p.out : (uintptr_t)sums) & 31) == 0;
 #pragma unroll 1
         for (int q = 0; q < D; q += 32) {
           float o[32];
           tc_ld32_issue(trow + TA_O + q, o);
           tc_wait_ld();
-          if (live && whole) {
+          if (live && whole && !p.raw) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] *= f.own;
+            if (p.prefix) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 4) {
+                float x[4] = {o[k], o[k + 1], o[k + 2], o[k + 3]};
+                add_prefix4(p.prefix + at * D + q + k, f.prefix, x);
+                o[k] = x[0]; o[k + 1] = x[1]; o[k + 2] = x[2]; o[k + 3] = x[3];
+              }
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               uint32_t y[8];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) y[k] = pack_bf16(o[16 * h + 2 * k] * inv, o[16 * h + 2 * k + 1] * inv);
+              for (int k = 0; k < 8; ++k) y[k] = pack_bf16(o[16 * h + 2 * k], o[16 * h + 2 * k + 1]);
               store32(static_cast<bf16*>(p.out) + at * D + q + 16 * h, y, sector);
             }
           } else if (live) {
@@ -430,11 +442,12 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
               uint32_t y[8];
 #pragma unroll
               for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(o[8 * h + k]);
-              store32(part + rl * D + q + 8 * h, y, sector);
+              store32(sums + q + 8 * h, y, sector);
             }
           }
         }
-        if (live && whole && p.lse) p.lse[at] = l == 0.f ? -INFINITY : 0.69314718056f * (m + log2f(l));
+        if (live && whole && !p.raw && p.lse) p.lse[at] = f.lse;
+        if (live && whole && p.raw) p.raw_ml[at] = make_float2(m, l);
         if (live && !whole) *reinterpret_cast<float2*>(part + TA_ROWS * D + 2 * rl) = make_float2(m, l);
       }
       tc_fence_before();                                     // before the next segment's first P
@@ -451,7 +464,7 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
     int u = ps.u;                                            // the unit to request next
     int page;                                                // its page of that unit
     auto pages = [&]() {
-      const int at = ps.bad ? 0 : min(u * TA_UNIT + tok, ps.L - 1);
+      const int at = ps.bad ? 0 : max(min(u * TA_UNIT + tok, ps.L - 1), 0);
       page = (int)load_now(reinterpret_cast<const uint32_t*>(p.table) + (size_t)ps.b * p.stride + (at >> page_bits));
     };
     struct Codes {
