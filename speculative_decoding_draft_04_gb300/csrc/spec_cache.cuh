@@ -72,12 +72,14 @@ struct Group4 {
 // Rounds x (which it overwrites) under the cache's scale g.  True: an element was
 // not finite.
 __device__ __forceinline__ bool round_group(float (&x)[16], float g, Group4& out) {
-  float amax = 0.f;                                      // of the numbers: a NaN is passed over
-  bool odd = false;
+  float amax = 0.f;
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    amax = fmaxf(amax, fabsf(x[e]));
-    odd |= !(fabsf(x[e]) <= 3.402823466e38f);
+  for (int e = 0; e < 16; ++e) asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(fabsf(x[e])));
+  const bool odd = !(amax <= 3.402823466e38f);
+  if (amax != amax) {                                    // of the numbers: a NaN is passed over
+    amax = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
   }
   const float tq = __fdiv_rn(amax, __fmul_rn(6.f, g));
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(out.scale) : "f"(0.f), "f"(tq));

@@ -6,10 +6,9 @@
 //   inv = 1 / sqrt(mean x^2 + eps),  y = (x inv) w
 //   y_a' = y_a c - y_b s,  y_b' = y_b c + y_a s
 //
-// The sum of squares is kept in double-float (Dot2) and inv is its rounded
-// reciprocal root, so that all of it has one value in fp32 whatever the order of
-// the sum: a 4-bit code is decided by the last bit of a key that lies next to a
-// border.
+// The sum of squares is kept in double-float and inv is its rounded reciprocal root,
+// so that all of it has one value in fp32 whatever the order of the sum: a 4-bit code
+// is decided by the last bit of a key that lies next to a border.
 //
 // A thread has 32 elements of a head, two groups of 16 that one scale each
 // describes in the cache: groups g and g + R / 32 where pairs are halves apart, so
@@ -53,8 +52,67 @@ __device__ __forceinline__ float root_reciprocal(df v) {
   return rn_fma(r, rn_mul(0.5f, e), r);
 }
 
+// The sum of a head's squares over its LANES lanes, 32 elements each, in double-float.
+// A plain sum first gives a power of two s0 above twice the sum.  Added to s0, every
+// partial sum stays within [s0, 2 s0), so what an addition rounds away is exact as
+// fma(x, x, s - s'), and the partial sums less s0 add up without rounding.
+template <int LANES>
+__device__ __forceinline__ df sum_of_squares(const float (&a)[16], const float (&b)[16]) {
+  float pa = 0.f, pb = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    pa = fmaf(a[i], a[i], pa);
+    pb = fmaf(b[i], b[i], pb);
+  }
+  float plain = pa + pb;
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) plain += __shfl_xor_sync(0xffffffffu, plain, o);
+  const float s0 = __uint_as_float((__float_as_uint(plain) & 0x7f800000u) + (2u << 23));
+  float sa = s0, sb = s0, ca = 0.f, cb = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float ta = rn_fma(a[i], a[i], sa), tb = rn_fma(b[i], b[i], sb);
+    ca = rn_add(ca, rn_fma(a[i], a[i], rn_sub(sa, ta)));
+    cb = rn_add(cb, rn_fma(b[i], b[i], rn_sub(sb, tb)));
+    sa = ta;
+    sb = tb;
+  }
+  float hi = rn_add(rn_sub(sa, s0), rn_sub(sb, s0)), lo = rn_add(ca, cb);
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) {
+    hi = rn_add(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    lo = rn_add(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+  }
+  return two_sum_df(hi, lo);
+}
+
+// Sixteen elements as they are in memory.
+template <class DT>
+struct Raw16 {
+  uint4 v[sizeof(DT)];
+  __device__ __forceinline__ void load(const DT* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(DT); ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void read(float (&x)[16]) const {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(DT); ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (sizeof(DT) == 2) {
+          x[8 * (i & 1) + 2 * k] = __uint_as_float(w[k] << 16);
+          x[8 * (i & 1) + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        } else {
+          x[4 * i + k] = __uint_as_float(w[k]);
+        }
+      }
+    }
+  }
+};
+
 template <int D, class DT>
-__global__ void __launch_bounds__(ROTARY_THREADS) rotary_append_kernel(const __grid_constant__ RotaryParams p) {
+__global__ void __launch_bounds__(ROTARY_THREADS, sizeof(DT) == 2 ? 4 : 3) rotary_append_kernel(const __grid_constant__ RotaryParams p) {
   constexpr int LANES = D / 32, HEADS = 32 / LANES;          // lanes a head, heads a warp
   const int lane = threadIdx.x & 31, j = lane % LANES;
   const long long item = (long long)blockIdx.x * (ROTARY_THREADS / 32) + (threadIdx.x >> 5);
@@ -62,6 +120,24 @@ __global__ void __launch_bounds__(ROTARY_THREADS) rotary_append_kernel(const __g
   const int t = (int)(item / runs), c0 = (int)(item - (long long)t * runs) * p.per_warp;
   if (t >= p.T) return;
   const int total = p.Hq + 2 * p.Hkv;
+  const bool apart = !p.interleaved && 32 * j < p.R, turn = 32 * j < p.R;
+  // the thread's two groups of elements, and its pairs of the rotation
+  const int ea = apart ? 16 * j : 32 * j, eb = apart ? p.R / 2 + 16 * j : 32 * j + 16;
+  // of the heads that come next: the first ones are requested before slot and position
+  // are known, later ones (bf16: fp32 has no registers for them) while others are worked on
+  constexpr bool AHEAD = sizeof(DT) == 2;
+  Raw16<DT> ra, rb;
+  auto request = [&](int c) {
+    const int head = c * HEADS + lane / LANES;
+    if (head >= total) return;
+    const int kind = head < p.Hq ? 0 : head < p.Hq + p.Hkv ? 1 : 2;
+    const int h = kind == 0 ? head : kind == 1 ? head - p.Hq : head - p.Hq - p.Hkv;
+    const DT* src = static_cast<const DT*>(p.x[kind]) + t * p.row[kind] + h * p.head[kind];
+    ra.load(src + ea);
+    rb.load(src + eb);
+  };
+  const int c1 = min(c0 + p.per_warp, p.chunks);
+  request(c0);
   const int slot = __ldg(p.slots + t), position = __ldg(p.positions + t);
   const bool skip = slot == -1;
   const bool bad_slot = !skip && (slot < 0 || slot >= p.num_slots);
@@ -70,9 +146,6 @@ __global__ void __launch_bounds__(ROTARY_THREADS) rotary_append_kernel(const __g
     set_status(p.status, (bad_slot ? SPEC_DEV_BAD_SLOT : 0) | (bad_position ? SPEC_DEV_BAD_POSITION : 0));
   const bool bad = bad_slot || bad_position;
 
-  // the thread's two groups of elements, and its pairs of the rotation
-  const bool apart = !p.interleaved && 32 * j < p.R, turn = 32 * j < p.R;
-  const int ea = apart ? 16 * j : 32 * j, eb = apart ? p.R / 2 + 16 * j : 32 * j + 16;
   float cs[32];
   if (turn && !skip && !bad) {
     const float4* r = reinterpret_cast<const float4*>(p.rope + (long long)position * p.R + 32 * j);
@@ -83,11 +156,12 @@ __global__ void __launch_bounds__(ROTARY_THREADS) rotary_append_kernel(const __g
     }
   }
 
-  for (int c = c0; c < min(c0 + p.per_warp, p.chunks); ++c) {
+  for (int c = c0; c < c1; ++c) {
     const int head = c * HEADS + lane / LANES;
     const int kind = head < p.Hq ? 0 : head < p.Hq + p.Hkv ? 1 : 2;
     const int h = kind == 0 ? head : kind == 1 ? head - p.Hq : head - p.Hq - p.Hkv;
     const bool live = head < total;
+    if (!AHEAD && c > c0) request(c);
     float a[16], b[16];
     if (skip || bad) {                                       // the whole warp
       if (!live) continue;
@@ -108,27 +182,18 @@ __global__ void __launch_bounds__(ROTARY_THREADS) rotary_append_kernel(const __g
       }
       continue;
     }
-    const DT* src = static_cast<const DT*>(p.x[kind]) + t * p.row[kind] + h * p.head[kind];
     if (live) {
-      load16(src + ea, a);
-      load16(src + eb, b);
+      ra.read(a);
+      rb.read(b);
     } else {
 #pragma unroll
       for (int i = 0; i < 16; ++i) a[i] = b[i] = 1.f;
     }
+    if (AHEAD && c + 1 < c1) request(c + 1);
     // ---- norm
     const void* weight = kind == 2 ? nullptr : p.weight[kind];
     if (__any_sync(0xffffffffu, weight != nullptr)) {
-      DdDot sum;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        sum.add(a[i], a[i]);
-        sum.add(b[i], b[i]);
-      }
-      df v = sum.value();
-#pragma unroll
-      for (int o = 1; o < LANES; o <<= 1)
-        v = dd_add(v, df{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
+      df v = sum_of_squares<LANES>(a, b);
       v = dd_add_f(df{v.hi * (1.f / D), v.lo * (1.f / D)}, p.eps);
       float inv = root_reciprocal(v);
       // squares that leave the range of fp32: the sum in 64 bits
@@ -211,7 +276,10 @@ template <int D, class DT>
 cudaError_t launch_rotary(RotaryParams p, int sms, cudaStream_t st) {
   constexpr int HEADS = 1024 / D;
   p.chunks = (p.Hq + 2 * p.Hkv + HEADS - 1) / HEADS;
-  p.per_warp = 1;
+  // a bf16 warp goes on to further heads of its token where there are warps enough
+  int parts = p.chunks;
+  while (sizeof(DT) == 2 && parts > 1 && (long long)p.T * (parts - 1) >= 32LL * sms) --parts;
+  p.per_warp = (p.chunks + parts - 1) / parts;
   const long long runs = (p.chunks + p.per_warp - 1) / p.per_warp;
   const long long warps = runs * p.T;
   const long long ctas = (warps + ROTARY_THREADS / 32 - 1) / (ROTARY_THREADS / 32);
