@@ -1,6 +1,7 @@
 """A few cycles of a server with a small random target model on one GPU:
-prompts into the paged 4-bit cache, then draft, target pass over the block,
-verification and log probabilities of the emitted tokens.
+prompts into the paged 4-bit cache, a first token drawn from each, then draft,
+target pass over the block, verification and log probabilities of the emitted
+tokens.
 
     python examples/served_cycle.py [--requests 8] [--cycles 4]
 
@@ -20,9 +21,10 @@ from speculative_decoding_draft_04_gb300 import engine, workloads
 
 
 class Target:
-    """Layers of attention over the cache with residual sums, random weights."""
+    """Layers of attention over the cache (heads normed and rotated by position)
+    with residual sums, random weights."""
 
-    def __init__(self, V, width, layers, Hq, Hkv, D, gen):
+    def __init__(self, V, width, layers, Hq, Hkv, D, longest, gen):
         def w(*shape):
             return (torch.randn(shape, generator=gen, device="cuda") * shape[0] ** -0.5).bfloat16()
         self.Hq, self.Hkv, self.D = Hq, Hkv, D
@@ -30,6 +32,8 @@ class Target:
         self.qkv = [w(width, (Hq + 2 * Hkv) * D) for _ in range(layers)]
         self.proj = [w(Hq * D, width) for _ in range(layers)]
         self.head = w(width, V)
+        ones = [torch.ones(D, dtype=torch.bfloat16, device="cuda") for _ in range(layers)]
+        self.rotary = engine.Rotary.table(longest, D, q_weight=ones, k_weight=ones)
 
     def __call__(self, tokens, c, last=None):
         """Logits of the packed rows (of the rows ``last`` only, where given)."""
@@ -38,7 +42,7 @@ class Target:
         for i, (wi, wo) in enumerate(zip(self.qkv, self.proj)):
             y = (torch.nn.functional.rms_norm(x, x.shape[1:]) @ wi).view(T, Hq + 2 * Hkv, D)
             o = torch.zeros((T, Hq, D), dtype=x.dtype, device=x.device)
-            engine.attend(c, i, y[:, :Hq], y[:, Hq:Hq + Hkv], y[:, Hq + Hkv:], o)
+            engine.attend(c, i, y[:, :Hq], y[:, Hq:Hq + Hkv], y[:, Hq + Hkv:], o, rotary=self.rotary)
             x = x + o.view(T, Hq * D) @ wo
         x = x if last is None else x[last]
         return torch.nn.functional.rms_norm(x, x.shape[1:]) @ self.head
@@ -52,23 +56,25 @@ def serve(requests=8, cycles=4, prompt=100, gamma=7, V=32000, width=512, layers=
     for its block emits nothing in that cycle and goes on when there are."""
     gen = torch.Generator("cuda").manual_seed(seed)
     B, n = requests, gamma + 1
-    model = Target(V, width, layers, Hq, Hkv, D, gen)
+    most = prompt + B + (cycles + 1) * n                      # tokens of the longest request
+    model = Target(V, width, layers, Hq, Hkv, D, most, gen)
     w = workloads.make_workload(workloads.config("C1", B=B, V=V, gamma=gamma, target=("normal", 0.5),
                                                noise=("fixed", 0.5)))
     d = engine.DeviceWorkload.from_workload(w)
     b = engine.Buffers.for_workload(d)
     l = engine.DeviceLogprobs.allocate(B, n, V, K=top)
-    most = prompt + B + (cycles + 1) * n                      # tokens of the longest request
     rows = B * prompt + B * (B - 1) // 2
     c = engine.DeviceCache.allocate(B, layers, Hq, Hkv, D, page_size, pages or B * -(-most // page_size), most,
                                     max(rows, B * n), [0.01] * layers, [0.01] * layers)
-    # prompts, one token longer from request to request; the last token of each
-    # becomes the first anchor
+    # prompts, one token longer from request to request; the first anchor is drawn
+    # from the logits of each one's last token
     held = torch.arange(prompt, prompt + B, dtype=torch.int32, device="cuda")
     tokens = torch.randint(0, V, (rows,), generator=gen, device="cuda", dtype=torch.int32)
     engine.make_room(c, held)
     first = model(tokens, c, last=(c.row_ptr[1:] - 1).long())
-    d.anchor.copy_(first.argmax(-1))
+    drawn = engine.DeviceSampling.allocate(B, top_k=50, top_p=0.95)
+    engine.sample(first[:, None], torch.rand((B, 1), generator=gen, device="cuda"), d.temperature, drawn)
+    d.anchor.copy_(drawn.tokens[:, 0])
     block = torch.full((B,), n, dtype=torch.int32, device="cuda")
 
     row = torch.arange(B * n, device="cuda")
@@ -93,7 +99,7 @@ def serve(requests=8, cycles=4, prompt=100, gamma=7, V=32000, width=512, layers=
         newest = b.out_tokens.gather(1, kept.clamp(min=0)[:, None].long())[:, 0]
         d.anchor.copy_(torch.where(kept < 0, d.anchor, newest))
         out.append((b.out_tokens.clone(), l.logprob.clone()))
-    words = [engine.status_words(t)[0] for t in (b.dstatus, b.vstatus, c.status, l.status)]
+    words = [engine.status_words(t)[0] for t in (b.dstatus, b.vstatus, c.status, l.status, drawn.status)]
     words[2] &= ~256                                          # pages that were not there
     if any(words):
         raise RuntimeError(f"status words {words}")

@@ -700,7 +700,9 @@ int32_t spec_logprobs(const spec_logprobs_args* args, spec_stream_t stream);
  * outputs, with the bit, for u outside [0, 1), top_p or min_p outside [0, 1]
  * (SPEC_DEV_BAD_FILTER), a temperature not finite and > 0 (SPEC_DEV_BAD_TEMP)
  * and a row with a NaN, +inf or only -inf (SPEC_DEV_BAD_LOGIT).
- * Rows as in spec_logprobs; 1 <= B * n <= 2^20, 1 <= V < 2^24.               */
+ * Rows: element (b, j, v) at logits[b * b_stride + j * row_stride + v]; any V,
+ * strides and address of an element.  1 <= B * n <= 2^20, 1 <= V < 2^24.
+ * Temperatures below 2^-100 count as that.                                   */
 typedef struct {
   int32_t B, n, V, dtype;
   const void* logits;

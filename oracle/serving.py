@@ -178,3 +178,59 @@ def logprobs(x: np.ndarray, T: float, token: int, K: int):
     H = lz - math.fsum(p * d[fin])
     ids = np.lexsort((np.arange(len(raw)), -raw))[:K]
     return d[token] - lz, H, ids, d[ids] - lz, math.fsum(p * d[fin] ** 2)
+
+
+# ------------------------------------------------------------- sampling
+
+def sample(x: np.ndarray, T: float, u: float, top_k: int = 0, top_p: float = 1.0, min_p: float = 0.0):
+    """token, logprob, kept of one row of logits, and how near the nearest border is that
+    decided them, as a part of the mass.  None: no distribution."""
+    raw = x.astype(np.float64)
+    if np.isnan(raw).any() or not math.isfinite(raw.max()):
+        return None
+    order = np.lexsort((np.arange(len(raw)), -raw))
+    order = order[np.isfinite(raw[order])]
+    if top_k > 0:
+        order = order[:top_k]
+    w = np.exp((raw - raw.max()) / T)
+    near = math.inf
+    z = math.fsum(w[order])
+    before = np.concatenate([[0.0], np.cumsum(w[order])[:-1]])
+    n = len(order)
+    if top_p < 1:
+        n = min(n, int((before < top_p * z).sum()))
+        near = min(near, float(np.abs(before[1:] - top_p * z).min(initial=math.inf)) / z)
+    n = min(n, int((w[order] >= min_p).sum()))
+    if min_p > 0:
+        off = np.abs(w[order] - min_p)
+        near = min(near, float(off[off > 0].min(initial=math.inf)) / z)
+    kept = np.sort(order[:max(1, n)])
+    f = np.cumsum(w[kept])
+    z = math.fsum(w[kept])
+    at = min(int((f <= u * z).sum()), len(kept) - 1)
+    near = min(near, float(np.abs(f - u * z).min()) / z)
+    token = int(kept[at])
+    return token, (raw[token] - raw.max()) / T - math.log(z), len(kept), near
+
+
+# ------------------------------------------------------------- norm and rotation
+
+def rotated(x: np.ndarray, rows: np.ndarray, weight=None, eps: float = 1e-6, interleaved: bool = False) -> np.ndarray:
+    """fp32 heads x [T, H, D], normed with a weight and their first elements rotated by rows
+    [T, R / 2, 2] (cosine, sine); every product and sum rounded to fp32, the norm's factor once."""
+    f = np.float32
+    with np.errstate(all="ignore"):
+        y = x.astype(f)
+        if weight is not None:
+            mean = (x.astype(np.float64) ** 2).mean(-1, keepdims=True)
+            y = (y * (1 / np.sqrt(mean + np.float64(f(eps)))).astype(f)) * weight.astype(f)
+        R = 2 * rows.shape[1]
+        c, s = rows[:, None, :, 0].astype(f), rows[:, None, :, 1].astype(f)
+        a, b = (y[..., 0:R:2], y[..., 1:R:2]) if interleaved else (y[..., :R // 2], y[..., R // 2:R])
+        out = y.copy()
+        p, q = a * c - b * s, b * c + a * s
+        if interleaved:
+            out[..., 0:R:2], out[..., 1:R:2] = p, q
+        else:
+            out[..., :R // 2], out[..., R // 2:R] = p, q
+    return out

@@ -25,7 +25,7 @@ ARGS = os.path.join(HERE, "_args" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARGS_FOR = os.path.join(OBJDIR, "args_for.txt")     # what ARGS was built for
 SOURCES = ["spec_abi.cu", "spec_draft.cu", "spec_draft_slice.cu", "spec_verify.cu",
            "spec_verify_slice.cu", "spec_verify_redecide.cu", "spec_refine.cu", "spec_report.cu",
-           "spec_sched.cu", "spec_tree.cu", "spec_tables.cu", "spec_cache.cu", "spec_attention.cu", "spec_attention_tc.cu",
+           "spec_sched.cu", "spec_tree.cu", "spec_tables.cu", "spec_cache.cu", "spec_attention.cu", "spec_prefix.cu",
            "spec_logprobs.cu", "spec_rotary.cu", "spec_sample.cu"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 NVCC_FLAGS = [ARCH, "-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",

@@ -927,7 +927,8 @@ int32_t spec_sample(const spec_sample_args* a, spec_stream_t stream) {
   if (a->B < 1 || a->n < 1 || (int64_t)a->B * a->n > (1 << 20) || a->V < 1 || a->V >= (1 << 24)) return SPEC_EINVAL;
   if (a->dtype != SPEC_F32 && a->dtype != SPEC_BF16) return SPEC_EUNSUPPORTED;
   if (!a->logits || !a->u || !a->tokens || !a->dev_status) return SPEC_EINVAL;
-  if (!aligned(a->logits, 16) || !aligned(a->u, 4) || !aligned(a->temperature, 4) || !aligned(a->top_k, 4) ||
+  if (!aligned(a->logits, a->dtype == SPEC_BF16 ? 2 : 4) || !aligned(a->u, 4) || !aligned(a->temperature, 4) ||
+      !aligned(a->top_k, 4) ||
       !aligned(a->top_p, 4) || !aligned(a->min_p, 4) || !aligned(a->tokens, 4) || !aligned(a->logprob, 4) ||
       !aligned(a->kept, 4) || !aligned(a->dev_status, 4))
     return SPEC_EALIGN;

@@ -23,18 +23,21 @@ struct AttnParams {
   float* lse;
   uint32_t* status;
   void* ws;
-  // The pass over shared prefixes: "requests" are groups of requests, whose rows see
+  // PASS_PREFIX, over shared prefixes: "requests" are groups of requests, whose rows see
   // every token, and sums are left unnormalised for the pass over own tokens.
-  const int* cut;                         // [B+1] first request of each group (null: not that pass)
+  const int* cut;                         // [B+1] first request of each group
   int members;                            // requests of all groups
   float* raw;                             // [T][Hq][D] sums, and (maximum, sum of p) a row
   float2* raw_ml;
   int* ranges;                            // 1 where cut and row_ptr cover every row once, else 0
-  // The pass over own tokens, after it: what to add to each row's sums.
-  const float* prefix;                    // null: nothing
+  // PASS_OWN, over own tokens, after it: what to add to each row's sums.
+  const float* prefix;
   const float2* prefix_ml;
   const int* prefix_ranges;
 };
+
+// What a launch of the kernels is for.
+enum { PASS_PLAIN, PASS_PREFIX, PASS_OWN };
 
 constexpr int AT_WARPS = 8;               // workspace slots: AT_MAX_CTAS * AT_WARPS workers at most
 constexpr int AT_UNIT = 32;               // tokens
@@ -59,17 +62,18 @@ struct AttnSeg {
   int b, h, tile, u, nu;                  // units u .. nu - 1 are left
   int n, r0, L;
   bool bad;
-  __device__ __forceinline__ int context(const AttnParams& p) const { return p.cut ? L : L - n; }   // tokens before the new ones
+  template <int PASS>
+  __device__ __forceinline__ int context() const { return PASS == PASS_PREFIX ? L : L - n; }   // tokens before the new ones
 };
 
 // Units of request b over all heads and row tiles (0: nothing to do).  LEAD: what
 // a segment costs besides its units, counted as units ahead of them.
-template <int ROWS, int UNIT, int LEAD>
+template <int PASS, int ROWS, int UNIT, int LEAD>
 __device__ __forceinline__ long long attn_work(const AttnParams& p, int b, int& n, int& r0, int& L, int& tiles,
                                                int& nu, bool& bad, bool& outside) {
   int b0 = b, b1 = b + 1;
   outside = false;
-  if (p.cut) {
+  if (PASS == PASS_PREFIX) {
     b0 = __ldg(p.cut + b);
     b1 = __ldg(p.cut + b + 1);
     outside = b0 < 0 || b1 < b0 || b1 > p.members;
@@ -86,7 +90,7 @@ __device__ __forceinline__ long long attn_work(const AttnParams& p, int b, int& 
     tiles = nu = 0;
     return 0;
   }
-  bad = L < (p.cut ? 0 : n) || L > (1 << 30) || L > (long long)p.stride * p.P;
+  bad = L < (PASS == PASS_PREFIX ? 0 : n) || L > (1 << 30) || L > (long long)p.stride * p.P;
   tiles = (n * p.G + ROWS - 1) / ROWS;
   nu = bad || L == 0 ? 1 : (L + UNIT - 1) / UNIT;          // no prefix: one unit of which nothing is seen
   return (long long)p.Hkv * tiles * (nu + LEAD);
@@ -95,7 +99,7 @@ __device__ __forceinline__ long long attn_work(const AttnParams& p, int b, int& 
 // Units before each group of requests, by the first THREADS threads of a CTA
 // (whole warps; the caller synchronises them before and after): s_pre[THREADS + 1],
 // s_scan[THREADS / 32].  A group is ceil(B / THREADS) requests.
-template <int ROWS, int UNIT, int THREADS, int LEAD = 0, class Sync>
+template <int PASS, int ROWS, int UNIT, int THREADS, int LEAD = 0, class Sync>
 __device__ __forceinline__ long long attn_prefix(const AttnParams& p, long long* s_pre, long long* s_scan, Sync sync) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int items = (p.B + THREADS - 1) / THREADS;
@@ -106,7 +110,7 @@ __device__ __forceinline__ long long attn_prefix(const AttnParams& p, long long*
     if (b >= p.B) break;
     int n, r0, L, tiles, nu;
     bool bad, outside;
-    mine += attn_work<ROWS, UNIT, LEAD>(p, b, n, r0, L, tiles, nu, bad, outside);
+    mine += attn_work<PASS, ROWS, UNIT, LEAD>(p, b, n, r0, L, tiles, nu, bad, outside);
     flag |= bad || outside;
   }
   long long v = mine;
@@ -126,7 +130,7 @@ __device__ __forceinline__ long long attn_prefix(const AttnParams& p, long long*
   s_pre[tid] = before + v - mine;
   if (tid == 0) s_pre[THREADS] = all;
   if (flag && blockIdx.x == 0) set_status(p.status, SPEC_DEV_BAD_LEN);
-  if (p.ranges && blockIdx.x == 0) {                       // do the groups cover every request's rows once
+  if (PASS == PASS_PREFIX && blockIdx.x == 0) {                       // do the groups cover every request's rows once
     bool ok = true;
     for (int b = tid; b <= p.members; b += THREADS) {
       const int r = __ldg(p.row_ptr + b);
@@ -155,8 +159,9 @@ __device__ __forceinline__ long long attn_prefix(const AttnParams& p, long long*
 struct AttnRow {
   float own, prefix, lse;
 };
+template <int PASS>
 __device__ __forceinline__ AttnRow attn_row(const AttnParams& p, size_t at, float m, float sum) {
-  if (!p.prefix) return {sum == 0.f ? 0.f : p.v_scale / sum, 0.f, sum == 0.f ? -INFINITY : 0.69314718056f * (m + log2f(sum))};
+  if (PASS == PASS_PLAIN) return {sum == 0.f ? 0.f : p.v_scale / sum, 0.f, sum == 0.f ? -INFINITY : 0.69314718056f * (m + log2f(sum))};
   const float2 v = __ldcg(p.prefix_ml + at);
   const float top = fmaxf(m, v.x), ref = top == -INFINITY ? 0.f : top;
   const float fa = exp2f(m - ref), fb = exp2f(v.x - ref);
@@ -167,7 +172,7 @@ __device__ __forceinline__ AttnRow attn_row(const AttnParams& p, size_t at, floa
 }
 
 // The segment that holds unit `pos` (below the total); LEAD more units to `u`.
-template <int ROWS, int UNIT, int THREADS, int LEAD = 0>
+template <int PASS, int ROWS, int UNIT, int THREADS, int LEAD = 0>
 __device__ __forceinline__ AttnSeg attn_locate(const AttnParams& p, const long long* s_pre, long long pos) {
   const int items = (p.B + THREADS - 1) / THREADS;
   int lo = 0, hi = THREADS;
@@ -180,7 +185,7 @@ __device__ __forceinline__ AttnSeg attn_locate(const AttnParams& p, const long l
   int tiles;
   for (int b = lo * items;; ++b) {
     bool outside;
-    const long long w = attn_work<ROWS, UNIT, LEAD>(p, b, s.n, s.r0, s.L, tiles, s.nu, s.bad, outside);
+    const long long w = attn_work<PASS, ROWS, UNIT, LEAD>(p, b, s.n, s.r0, s.L, tiles, s.nu, s.bad, outside);
     if (left < w) {
       s.b = b;
       break;
@@ -293,8 +298,7 @@ __device__ __forceinline__ void store4(float* p, const float* x) {
 }
 
 // x + f times four elements of a prefix's sums.
-__device__ __forceinline__ void add_prefix4(const float* from, float f, float (&x)[4]) {
-  const float4 v = __ldcg(reinterpret_cast<const float4*>(from));
+__device__ __forceinline__ void add_prefix4(const float4& v, float f, float (&x)[4]) {
   x[0] = fmaf(f, v.x, x[0]);
   x[1] = fmaf(f, v.y, x[1]);
   x[2] = fmaf(f, v.z, x[2]);
@@ -309,14 +313,14 @@ __device__ __forceinline__ int k_order(int t, int s) {
 
 // The segment after one that ended, whose first unit is `pos`: most often the
 // same request's.
-template <int ROWS, int UNIT, int THREADS, int LEAD = 0>
+template <int PASS, int ROWS, int UNIT, int THREADS, int LEAD = 0>
 __device__ __forceinline__ AttnSeg attn_next(const AttnParams& p, const long long* s_pre, const AttnSeg& seg, long long pos) {
   AttnSeg s = seg;
   s.u = 0;
   if (++s.tile * ROWS < s.n * p.G) return s;
   s.tile = 0;
   if (++s.h < p.Hkv) return s;
-  return attn_locate<ROWS, UNIT, THREADS, LEAD>(p, s_pre, pos);
+  return attn_locate<PASS, ROWS, UNIT, THREADS, LEAD>(p, s_pre, pos);
 }
 
 // The power of two that takes mx into [2^14, 2^15) (at most 2^120; 2^15 for 0,
@@ -328,8 +332,6 @@ __device__ __forceinline__ int query_exponent(float mx) {
 }
 __device__ __forceinline__ float power_of_2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126 .. 127
 
-// The kernel of 128-row tiles (bf16, D = 64 or 128).
-cudaError_t launch_cache_attention_tc(const AttnParams& p, int D, int sms, cudaStream_t st);
 
 // Adds the parts of the split segments: CTA (x, y) takes the segments that
 // begin at workers x, x + gridDim.x, .. and 1024 / D rows of each.  A part is
@@ -341,7 +343,7 @@ cudaError_t launch_cache_attention_tc(const AttnParams& p, int D, int sms, cudaS
 // Its launch overlaps the main kernel's end; 10 to 25 us by itself with cold
 // caches (two rows a CTA: 24 us where 14 are kept, for 1824 workers of 2 parts).
 constexpr int JOIN_THREADS = 256, JOIN_BATCH = 4;
-template <int D, int ROWS, class DT>
+template <int PASS, int D, int ROWS, class DT>
 __global__ void __launch_bounds__(JOIN_THREADS) cache_attention_join_kernel(const __grid_constant__ AttnParams p, int workers) {
   __shared__ float4 s_acc[JOIN_THREADS];
   __shared__ float2 s_ml[JOIN_THREADS];
@@ -412,14 +414,16 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_attention_join_kernel(cons
       const int r = s.tile * ROWS + rl;
       const int tok = r / p.G, hq = s.h * p.G + r - tok * p.G;
       const size_t at = (size_t)(s.r0 + tok) * p.Hq + hq;
-      if (p.raw) {
+      if (PASS == PASS_PREFIX) {
         *reinterpret_cast<float4*>(p.raw + at * D + d) = acc;
         if (d == 0) p.raw_ml[at] = ml;
         continue;
       }
-      const AttnRow f = attn_row(p, at, ml.x, ml.y);
+      float4 before = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (PASS == PASS_OWN) before = __ldcg(reinterpret_cast<const float4*>(p.prefix + at * D + d));
+      const AttnRow f = attn_row<PASS>(p, at, ml.x, ml.y);
       float x[4] = {acc.x * f.own, acc.y * f.own, acc.z * f.own, acc.w * f.own};
-      if (p.prefix) add_prefix4(p.prefix + at * D + d, f.prefix, x);
+      if (PASS == PASS_OWN) add_prefix4(before, f.prefix, x);
       store4(static_cast<DT*>(p.out) + at * D + d, x);
       if (d == 0 && p.lse) p.lse[at] = f.lse;
     }
@@ -428,7 +432,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_attention_join_kernel(cons
 
 // Launches the join after the main kernel of `ctas` CTAs x `per_cta` workers;
 // its launch overlaps the main kernel's end.
-template <int D, int ROWS, class DT>
+template <int PASS, int D, int ROWS, class DT>
 cudaError_t launch_attention_join(const AttnParams& p, int workers, int sms, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(workers < 4 * sms ? workers : 4 * sms, (ROWS * D / 4 + JOIN_THREADS - 1) / JOIN_THREADS);
@@ -439,7 +443,7 @@ cudaError_t launch_attention_join(const AttnParams& p, int workers, int sms, cud
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_attention_join_kernel<D, ROWS, DT>, p, workers);
+  return cudaLaunchKernelEx(&cfg, cache_attention_join_kernel<PASS, D, ROWS, DT>, p, workers);
 }
 
 }  // namespace spec

@@ -31,6 +31,8 @@
 // memory busy.  100 of 128 rows reach 0.4 PFLOP/s (72 to 80 us a call, by the
 // trees' lengths); 16-row tiles of mma.sync take 211 us for as many rows, decoding
 // every token seven times.  Eight prompts of 512 tokens take 102 us, of 2048 777.
+#pragma once
+
 #include <atomic>
 
 #include "spec_attention.cuh"
@@ -166,6 +168,7 @@ __device__ __forceinline__ uint32_t seen_word(const AttnParams& p, int d, int li
 // The segments of a CTA's share [pos, end), each with the units u .. u_end - 1 of
 // it that are the CTA's.  A share that ends inside a segment's lead has none of
 // its units, and one that begins there has it from its first unit on.
+template <int PASS>
 struct TaWalk {
   AttnSeg sg;
   int u_end;
@@ -173,7 +176,7 @@ struct TaWalk {
   __device__ __forceinline__ TaWalk(const AttnParams& p, const long long* s_pre, long long begin, long long end_)
       : pos(begin), end(end_) {
     if (pos < end) {
-      sg = attn_locate<TA_ROWS, TA_UNIT, TA_PREFIX, TA_LEAD>(p, s_pre, pos);
+      sg = attn_locate<PASS, TA_ROWS, TA_UNIT, TA_PREFIX, TA_LEAD>(p, s_pre, pos);
       pos -= sg.u;                                           // where the segment begins
       sg.u = max(sg.u - TA_LEAD, 0);
       cut();
@@ -188,13 +191,13 @@ struct TaWalk {
   __device__ __forceinline__ void next(const AttnParams& p, const long long* s_pre) {
     pos += TA_LEAD + sg.nu;
     if (pos < end) {
-      sg = attn_next<TA_ROWS, TA_UNIT, TA_PREFIX, TA_LEAD>(p, s_pre, sg, pos);
+      sg = attn_next<PASS, TA_ROWS, TA_UNIT, TA_PREFIX, TA_LEAD>(p, s_pre, sg, pos);
       cut();
     }
   }
 };
 
-template <int D>
+template <int PASS, int D>
 __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const __grid_constant__ AttnParams p) {
   using L = TaLayout<D>;
   constexpr int KSTEPS = D / 16, TASKS = D / 64;             // 64 elements each: a decoding thread's of a unit
@@ -216,7 +219,7 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
   }
   if (warp == 8) tc_alloc(&s_tmem, TA_COLS);
   if (tid < TA_PREFIX)
-    attn_prefix<TA_ROWS, TA_UNIT, TA_PREFIX, TA_LEAD>(p, s_pre, s_scan,
+    attn_prefix<PASS, TA_ROWS, TA_UNIT, TA_PREFIX, TA_LEAD>(p, s_pre, s_scan,
                                                       [] { asm volatile("barrier.cta.sync.aligned 3, 256;\n" ::: "memory"); });
   tc_fence_before();
   __syncthreads();
@@ -249,7 +252,7 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
   };
   AttnSplit split{0, -1, 0, 0, 0, 0, 0};
 
-  TaWalk walk(p, s_pre, begin, end);
+  TaWalk<PASS> walk(p, s_pre, begin, end);
   if (walk.done()) {
   } else if (warp < 4) {
     // ------------------------------------------------ softmax
@@ -282,7 +285,7 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
       const AttnSeg sg = walk.sg;
       const int u_first = sg.u, u_end = walk.u_end;
       const long long last = walk.pos + TA_LEAD + sg.nu - 1;   // the segment's last unit
-      const int ctx = sg.context(p);
+      const int ctx = sg.template context<PASS>();
       const bool live = ntok >= 0;
       const int tok = live ? ntok : 0, hq = nhq;
       // ---- this thread's query as 16-bit floats, scaled by a power of two so that
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
       fence_async_shared();
       arrive(bar + TB_Q);
       bool poison = sg.bad;                                  // a page outside the cache in this part
-      const int lim = live ? (p.cut ? sg.L : p.mask ? sg.r0 + tok : ctx + tok + 1) : -1;   // tokens it sees (causal), its packed row
+      const int lim = live ? (PASS == PASS_PREFIX ? sg.L : p.mask ? sg.r0 + tok : ctx + tok + 1) : -1;   // tokens it sees (causal), its packed row
       const bool some = __any_sync(0xffffffffu, live);
       float mref = -INFINITY, l = 0.f;
       for (int u = u_first; u < u_end; ++u, ++i) {
@@ -410,22 +413,25 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
       if (some) {
         const size_t at = (size_t)(sg.r0 + tok) * p.Hq + hq;
         AttnRow f{};
-        if (live && whole && !p.raw) f = attn_row(p, at, m, l);
-        float* const sums = !whole ? part + rl * D : p.raw + at * D;   // where they are kept as they are
-        const bool sector = ((whole && !p.raw ? (uintptr_t)p.out : (uintptr_t)sums) & 31) == 0;
+        if (live && whole && PASS != PASS_PREFIX) f = attn_row<PASS>(p, at, m, l);
+        float* const sums = PASS == PASS_PREFIX && whole ? p.raw + at * D : part + rl * D;   // where they are kept as they are
+        const bool sector = ((whole && PASS != PASS_PREFIX ? (uintptr_t)p.out : (uintptr_t)sums) & 31) == 0;
 #pragma unroll 1
         for (int q = 0; q < D; q += 32) {
           float o[32];
           tc_ld32_issue(trow + TA_O + q, o);
           tc_wait_ld();
-          if (live && whole && !p.raw) {
+          if (live && whole && PASS != PASS_PREFIX) {
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] *= f.own;
-            if (p.prefix) {
+            if (PASS == PASS_OWN) {
+              float4 before[8];                              // the prefix's sums of these columns
+#pragma unroll
+              for (int k = 0; k < 8; ++k) before[k] = __ldcg(reinterpret_cast<const float4*>(p.prefix + at * D + q) + k);
 #pragma unroll
               for (int k = 0; k < 32; k += 4) {
                 float x[4] = {o[k], o[k + 1], o[k + 2], o[k + 3]};
-                add_prefix4(p.prefix + at * D + q + k, f.prefix, x);
+                add_prefix4(before[k / 4], f.prefix, x);
                 o[k] = x[0]; o[k + 1] = x[1]; o[k + 2] = x[2]; o[k + 3] = x[3];
               }
             }
@@ -446,8 +452,8 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
             }
           }
         }
-        if (live && whole && !p.raw && p.lse) p.lse[at] = f.lse;
-        if (live && whole && p.raw) p.raw_ml[at] = make_float2(m, l);
+        if (live && whole && PASS != PASS_PREFIX && p.lse) p.lse[at] = f.lse;
+        if (live && whole && PASS == PASS_PREFIX) p.raw_ml[at] = make_float2(m, l);
         if (live && !whole) *reinterpret_cast<float2*>(part + TA_ROWS * D + 2 * rl) = make_float2(m, l);
       }
       tc_fence_before();                                     // before the next segment's first P
@@ -594,7 +600,7 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
 }
 
 namespace {
-template <int D>
+template <int PASS, int D>
 cudaError_t launch_tc(const AttnParams& p, int sms, cudaStream_t st) {
   using L = TaLayout<D>;
   static_assert(2 * (L::TOTAL + 5 * 1024) <= 227 * 1024, "two CTAs an SM");
@@ -604,7 +610,7 @@ cudaError_t launch_tc(const AttnParams& p, int sms, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !((sized.load(std::memory_order_relaxed) >> dev) & 1)) {
-    e = cudaFuncSetAttribute(cache_attention_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::TOTAL);
+    e = cudaFuncSetAttribute(cache_attention_tc_kernel<PASS, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::TOTAL);
     if (e != cudaSuccess) return e;
     if (dev < 64) sized.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
@@ -613,14 +619,15 @@ cudaError_t launch_tc(const AttnParams& p, int sms, cudaStream_t st) {
   long long ctas = 2LL * sms;
   if (ctas > AT_MAX_CTAS) ctas = AT_MAX_CTAS;
   if (ctas > units) ctas = units;
-  cache_attention_tc_kernel<D><<<(int)ctas, TA_THREADS, L::TOTAL, st>>>(p);
+  cache_attention_tc_kernel<PASS, D><<<(int)ctas, TA_THREADS, L::TOTAL, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_attention_join<D, TA_ROWS, bf16>(p, (int)ctas, sms, st);
+  return launch_attention_join<PASS, D, TA_ROWS, bf16>(p, (int)ctas, sms, st);
 }
 }  // namespace
 
+template <int PASS>
 cudaError_t launch_cache_attention_tc(const AttnParams& p, int D, int sms, cudaStream_t st) {
-  return D == 64 ? launch_tc<64>(p, sms, st) : launch_tc<128>(p, sms, st);
+  return D == 64 ? launch_tc<PASS, 64>(p, sms, st) : launch_tc<PASS, 128>(p, sms, st);
 }
 
 }  // namespace spec

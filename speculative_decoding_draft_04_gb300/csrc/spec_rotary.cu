@@ -197,13 +197,13 @@ __global__ void __launch_bounds__(ROTARY_THREADS, sizeof(DT) == 2 ? 4 : 3) rotar
       v = dd_add_f(df{v.hi * (1.f / D), v.lo * (1.f / D)}, p.eps);
       float inv = root_reciprocal(v);
       // squares that leave the range of fp32: the sum in 64 bits
-      if (__any_sync(0xffffffffu, weight && !(v.hi >= 1e-20f && v.hi <= 1e37f))) {
+      if (__any_sync(0xffffffffu, weight && !(v.hi >= 1e-20f && v.hi <= 1e35f))) {
         double wide = 0.;
 #pragma unroll
         for (int i = 0; i < 16; ++i) wide += (double)a[i] * a[i] + (double)b[i] * b[i];
 #pragma unroll
         for (int o = 1; o < LANES; o <<= 1) wide += __shfl_xor_sync(0xffffffffu, wide, o);
-        if (!(v.hi >= 1e-20f && v.hi <= 1e37f)) inv = (float)(1. / sqrt(wide / D + (double)p.eps));
+        if (!(v.hi >= 1e-20f && v.hi <= 1e35f)) inv = (float)(1. / sqrt(wide / D + (double)p.eps));
       }
       if (weight) {
         float w[16];

@@ -394,15 +394,136 @@ def make_room(c: DeviceCache, new_len, accept_len=None, stream=None) -> None:
     c.newest = new
 
 
-def attend(c: DeviceCache, layer: int, q, k, v, out, tree_mask=None, lse=None, stream=None) -> None:
+@dataclasses.dataclass
+class Rotary:
+    """What a target model does to queries and keys before attention: norms per
+    head (one weight of D elements a layer, or None) and the rotation by position,
+    rope [rows][R / 2][2] (cosine, sine)."""
+    rope: object
+    q_weight: object = None     # per layer
+    k_weight: object = None
+    eps: float = 1e-6
+    interleaved: bool = False
+
+    @classmethod
+    def table(cls, rows, R, base=10000.0, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+              device="cuda") -> "Rotary":
+        """Angles position * base^(-2 i / R), formed in float64."""
+        import torch
+        f = base ** (-2.0 * torch.arange(R // 2, dtype=torch.float64, device=device) / R)
+        a = torch.arange(rows, dtype=torch.float64, device=device)[:, None] * f
+        return cls(rope=torch.stack([torch.cos(a), torch.sin(a)], -1).float().contiguous(), q_weight=q_weight,
+                   k_weight=k_weight, eps=eps, interleaved=interleaved)
+
+
+@dataclasses.dataclass
+class Prefixes:
+    """Prefixes that groups of a cache's requests share.  The cache's last requests
+    hold them, one a group: they append the prefix like a prompt, and no tokens
+    afterwards (new_len 0, accept_len -1).  Requests group_ptr[g] ..
+    group_ptr[g + 1] - 1 begin with the tokens of holder g."""
+    requests: int               # the others of the cache
+    group_ptr: object           # int32 [groups + 1], ending in `requests`
+    group: object               # int64 [requests]: the group of each request
+    positions: object           # int32 [max_rows]: positions that count the prefix
+    workspace: object
+
+    @classmethod
+    def allocate(cls, c: DeviceCache, group_sizes, Hq) -> "Prefixes":
+        import torch
+        groups, requests = len(group_sizes), sum(group_sizes)
+        if requests + groups != c.kv_len.numel():
+            raise _lib.SpecError(f"{groups} groups of {requests} requests need a cache of {requests + groups}, "
+                                 f"not {c.kv_len.numel()}")
+        _, Hkv, _, bytes16 = c.layers[0].shape
+        size = _lib.spec_prefix_attention_workspace_bytes(c.slots.numel(), Hq, Hkv, bytes16 // 18)
+        if size == 0:
+            raise _lib.SpecError("unsupported heads for libspec")
+        sizes = torch.tensor(list(group_sizes), dtype=torch.int64)
+        ptr = torch.cat([torch.zeros(1, dtype=torch.int64), sizes.cumsum(0)])
+        o = dict(device=c.kv_len.device)
+        return cls(requests=requests, group_ptr=ptr.to(torch.int32).to(**o),
+                   group=torch.arange(groups).repeat_interleave(sizes).to(**o),
+                   positions=torch.zeros_like(c.positions), workspace=torch.empty(size, dtype=torch.uint8, **o))
+
+
+def place_after(c: DeviceCache, s: Prefixes, stream=None) -> None:
+    """Positions of the newest step's rows behind their prefixes (to be called
+    after make_room, before the step's layers)."""
+    import contextlib
+
+    import torch
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        row = torch.arange(c.positions.numel(), device=c.positions.device)
+        who = torch.searchsorted(c.row_ptr[1:s.requests + 1].long(), row, right=True).clamp(max=s.requests - 1)
+        before = c.kv_len[s.requests:][s.group[who]]
+        torch.where(c.positions < 0, c.positions, c.positions + before, out=s.positions)
+
+
+def attend(c: DeviceCache, layer: int, q, k, v, out, tree_mask=None, lse=None, stream=None,
+           rotary: Rotary | None = None, prefixes: Prefixes | None = None) -> None:
     """One layer's attention of the newest step's packed rows: their keys and
     values go into the cache, their queries over it.  q, k, v: [T][heads][D]
-    with T at most the rows that the step was made for."""
-    _lib.spec_cache_append(k, v, c.slots[:k.shape[0]], c.layers[layer], c.status, c.k_scale[layer],
-                           c.v_scale[layer], stream=stream)
-    _lib.spec_cache_attention(q, c.layers[layer], c.block_table, c.kv_len, c.row_ptr, out, c.status,
-                              c.workspace, c.softmax_scale, c.k_scale[layer], c.v_scale[layer],
-                              tree_mask=tree_mask, lse=lse, stream=stream)
+    with T at most the rows that the step was made for.  rotary: queries (in
+    place) and keys are normed and rotated first.  prefixes: the rows are the
+    sharing requests' (the holders have none in this step), each sees its
+    group's prefix before its own tokens."""
+    T = k.shape[0]
+    if rotary is None:
+        _lib.spec_cache_append(k, v, c.slots[:T], c.layers[layer], c.status, c.k_scale[layer],
+                               c.v_scale[layer], stream=stream)
+    else:
+        _lib.spec_rotary_append(q, k, v, (c if prefixes is None else prefixes).positions[:T], c.slots[:T],
+                                rotary.rope, q, c.layers[layer], c.status, c.k_scale[layer], c.v_scale[layer],
+                                q_weight=None if rotary.q_weight is None else rotary.q_weight[layer],
+                                k_weight=None if rotary.k_weight is None else rotary.k_weight[layer],
+                                eps=rotary.eps, interleaved=rotary.interleaved, stream=stream)
+    if prefixes is None:
+        _lib.spec_cache_attention(q, c.layers[layer], c.block_table, c.kv_len, c.row_ptr, out, c.status,
+                                  c.workspace, c.softmax_scale, c.k_scale[layer], c.v_scale[layer],
+                                  tree_mask=tree_mask, lse=lse, stream=stream)
+    else:
+        n = prefixes.requests
+        _lib.spec_prefix_attention(q, c.layers[layer], c.block_table[:n], c.kv_len[:n], c.row_ptr[:n + 1],
+                                   c.block_table[n:], c.kv_len[n:], prefixes.group_ptr, out, c.status,
+                                   prefixes.workspace, c.softmax_scale, c.k_scale[layer], c.v_scale[layer],
+                                   tree_mask=tree_mask, lse=lse, stream=stream)
+
+
+@dataclasses.dataclass
+class DeviceSampling:
+    """Settings of sampling (per request, each None for no limit) and what was
+    drawn."""
+    top_k: object
+    top_p: object
+    min_p: object
+    tokens: object
+    logprob: object
+    kept: object
+    status: object
+
+    @classmethod
+    def allocate(cls, B, n=1, top_k=None, top_p=None, min_p=None, device="cuda") -> "DeviceSampling":
+        """n tokens a request; settings: numbers, or one a request."""
+        import torch
+        o = dict(device=device)
+
+        def setting(x, dtype):
+            if x is None:
+                return None
+            return torch.broadcast_to(torch.as_tensor(x, dtype=dtype), (B,)).contiguous().to(device)
+        return cls(top_k=setting(top_k, torch.int32), top_p=setting(top_p, torch.float32),
+                   min_p=setting(min_p, torch.float32), tokens=torch.empty((B, n), dtype=torch.int32, **o),
+                   logprob=torch.empty((B, n), dtype=torch.float32, **o),
+                   kept=torch.empty((B, n), dtype=torch.int32, **o),
+                   status=torch.zeros(4, dtype=torch.int32, **o))
+
+
+def sample(logits, u, temperature, s: DeviceSampling, stream=None) -> None:
+    """Draw s.tokens [B][n] from logits [B][n][V] with uniform numbers u [B][n]
+    (-1: the row is skipped): the first tokens after prompts, or plain decoding."""
+    _lib.spec_sample(logits, u, s.tokens, s.status, temperature=temperature, top_k=s.top_k, top_p=s.top_p,
+                     min_p=s.min_p, logprob=s.logprob, kept=s.kept, stream=stream)
 
 
 @dataclasses.dataclass
