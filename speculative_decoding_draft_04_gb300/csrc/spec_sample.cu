@@ -230,7 +230,7 @@ struct SampleShared {
   u64 hist[SA_BINS / 2];                  // counts of 32 bits; 64-bit sums of half as many bins in a search
   u64 tile[SA_TILES];                     // kept mass
   alignas(16) float2 tab[SA_TABLE];
-  u64 scan[SA_WARPS];
+  u64 scan[SA_WARPS], ends[2][SA_WARPS];
   u64 before;                             // of the bin or tile that a search goes on in
   u64 sum[3];                             // of one CTA, read by the cluster: all, certainly kept, kept
   int bin[2], listed, at;
@@ -386,6 +386,12 @@ struct Sampler {
     return lane < C ? f(cl.map_shared_rank(&s, lane)) : none;
   }
 
+  // Adds w to a 64-bit bin, once for the lanes that add the same to the same one: 64-bit
+  // additions to one address go one after the other, and ties send thousands there.
+  __device__ __forceinline__ void add_to_bin(int bin, u64 w) const {
+    const uint32_t same = __match_any_sync(__activemask(), ((u64)bin << 44) | w);
+    if (__ffs(same) - 1 == lane) atomicAdd(&s.hist[bin], w * __popc(same));
+  }
   __device__ __forceinline__ void clear_bins() {
     for (int i = tid; i < SA_BINS / 2; i += SA_THREADS) s.hist[i] = 0;
   }
@@ -401,11 +407,11 @@ struct Sampler {
     return c;
   }
 
-  // The smallest key of [lo, hi] whose running sum passes `goal`, over the row, adding
-  // weight(x) of its entries.  False: no key does.
+  // The smallest key of [lo, hi] whose running sum, from `base` on, passes `goal`, over
+  // the row, adding weight(x) of its entries.  False: no key does.
   template <class Weight>
-  __device__ __forceinline__ bool search(u64 lo, u64 hi, u64 goal, Weight weight, u64& found) {
-    for (u64 base = 0;;) {
+  __device__ __forceinline__ bool search(u64 lo, u64 hi, u64 base, u64 goal, Weight weight, u64& found) {
+    for (;;) {
       const int bits = 64 - __clzll((long long)(hi - lo));
       const int shift = bits > SA_STEP_BITS ? bits - SA_STEP_BITS : 0;
       sync();                                             // the bins have been read
@@ -416,7 +422,7 @@ struct Sampler {
             const u64 k = key_of(x, v);
             if (k >= lo && k <= hi) {
               const u64 w = weight(x);
-              if (w) atomicAdd(&s.hist[(k - lo) >> shift], w);
+              if (w) add_to_bin((int)((k - lo) >> shift), w);
             }
           },
           [](int) {});
@@ -481,40 +487,56 @@ struct Sampler {
     return k;
   }
   // Of the list's n keys up to `most`: the first whose running sum, of weights after `base`
-  // or of ones, passes `goal`.  False: too many next to it.
-  __device__ __forceinline__ bool pick(const Weigh& weigh, int n, u64 most, bool weights, u64 base, u64 goal, u64& found) {
-    u64 own = ~0ull;
+  // or of ones, passes `goal`.
+  __device__ __forceinline__ u64 pick(const Weigh& weigh, int n, u64 most, bool weights, u64 base, u64 goal) {
+    constexpr int PER = SA_LIST / SA_THREADS, BINS = SA_BINS / 2;
+    u64 k[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int at = tid + i * SA_THREADS;
+      k[i] = at < n && s.sorted[at] <= most ? s.sorted[at] : ~0ull;
+    }
+    // while there are more than threads: the bin of their range in which the sum passes the
+    // goal, by values first, then (equal values, or values of one bin) by whole keys
     int left = n;
-    if (n <= SA_THREADS) {
-      if (tid < n && s.sorted[tid] <= most) own = s.sorted[tid];
-    } else {
-      // the bin of the list's range in which the sum passes the goal, and its keys
-      constexpr int PER = SA_LIST / SA_THREADS, BINS = SA_BINS / 2;
-      u64 k[PER], lo = ~0ull, hi = 0;
+    for (int round = 0; left > SA_THREADS; ++round) {
+      u64 lo = ~0ull, hi = 0;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const int at = tid + i * SA_THREADS;
-        k[i] = at < n && s.sorted[at] <= most ? s.sorted[at] : ~0ull;
         lo = k[i] < lo ? k[i] : lo;
         hi = k[i] != ~0ull && k[i] > hi ? k[i] : hi;
       }
-      // (values are enough for the bins)
-      if (tid < 2) s.bin[tid] = tid ? 0 : -1;                  // unsigned extremes
-      clear_bins();
-      __syncthreads();
-      const uint32_t first_value = __reduce_min_sync(0xffffffffu, (uint32_t)(lo >> p.idx_bits));
-      const uint32_t last_value = __reduce_max_sync(0xffffffffu, (uint32_t)(hi >> p.idx_bits));
-      if (lane == 0) {
-        atomicMin(reinterpret_cast<uint32_t*>(&s.bin[0]), first_value);
-        atomicMax(reinterpret_cast<uint32_t*>(&s.bin[1]), last_value);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        const u64 a = __shfl_xor_sync(0xffffffffu, lo, o), b = __shfl_xor_sync(0xffffffffu, hi, o);
+        lo = a < lo ? a : lo;
+        hi = b > hi ? b : hi;
       }
       __syncthreads();
-      const float top = of_descending<DT>((uint32_t)s.bin[0]), end = of_descending<DT>((uint32_t)s.bin[1]);
-      const float scale = (float)BINS / fminf(fmaxf(top - end, 1e-30f), -SA_LOWEST);
-      auto bin_of = [&](u64 key) { return min(__float2int_rz(rn_mul(rn_sub(top, value_of(key)), scale)), BINS - 1); };
+      if (lane == 0) {
+        s.ends[0][warp] = lo;
+        s.ends[1][warp] = hi;
+      }
+      clear_bins();
+      __syncthreads();
+#pragma unroll 1
+      for (int w = 0; w < SA_WARPS; ++w) {
+        lo = s.ends[0][w] < lo ? s.ends[0][w] : lo;
+        hi = s.ends[1][w] > hi ? s.ends[1][w] : hi;
+      }
+      const float top = value_of(lo), scale = (float)BINS / fminf(fmaxf(top - value_of(hi), 1e-30f), -SA_LOWEST);
+      const int bits = 64 - __clzll((long long)(hi - lo)), shift = bits > 10 ? bits - 10 : 0;
+      static_assert(BINS == 1 << 10, "ten bits of a key");
+      auto bin_of = [&](u64 key) {
+        return round == 0 ? min(__float2int_rz(rn_mul(rn_sub(top, value_of(key)), scale)), BINS - 1) : (int)((key - lo) >> shift);
+      };
 #pragma unroll
       for (int i = 0; i < PER; ++i)
-        if (k[i] != ~0ull) atomicAdd(&s.hist[bin_of(k[i])], weights ? weight_of(weigh, value_of(k[i])) : 1ull);
+        if (k[i] != ~0ull) add_to_bin(bin_of(k[i]), weights ? weight_of(weigh, value_of(k[i])) : 1ull);
+      if (tid == 0) {
+        s.bin[0] = -1;
+        s.bin[1] = 0;
+      }
       __syncthreads();
       const u64 h0 = s.hist[2 * tid], h1 = s.hist[2 * tid + 1];
       const u64 at0 = base + block_before(h0 + h1, s.scan).before, at1 = at0 + h0;
@@ -526,29 +548,41 @@ struct Sampler {
         s.bin[0] = 2 * tid + 1;
         s.before = at1;
       }
-      if (tid == 0) s.bin[1] = 0;
       __syncthreads();
       const int bin = s.bin[0];
+      if (bin < 0) break;                                    // the sum does not pass it here: min-p's floor lies above
       base = s.before;
+      int in_bin = 0;
 #pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (k[i] != ~0ull && bin_of(k[i]) == bin) {
-          const int to = atomicAdd(&s.bin[1], 1);
-          if (to < SA_THREADS) s.hist[to] = k[i];            // the bins have been read
-        }
+      for (int i = 0; i < PER; ++i) {
+        if (k[i] != ~0ull && bin_of(k[i]) != bin) k[i] = ~0ull;
+        in_bin += k[i] != ~0ull;
+      }
+      if (in_bin) atomicAdd(&s.bin[1], in_bin);
       __syncthreads();
       left = s.bin[1];
-      if (left > SA_THREADS) return false;
-      if (tid < left) own = s.hist[tid];
     }
+    // one a thread
+    __syncthreads();
+    if (tid == 0) s.bin[1] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (k[i] != ~0ull) {
+        const int to = atomicAdd(&s.bin[1], 1);
+        if (to < SA_THREADS) s.hist[to] = k[i];
+      }
+    __syncthreads();
+    left = min(s.bin[1], SA_THREADS);
+    u64 own = tid < left ? s.hist[tid] : ~0ull;
     own = sort_keys(own, left);
     const u64 w = own == ~0ull ? 0 : weights ? weight_of(weigh, value_of(own)) : 1;
     const u64 at = base + block_before(w, s.scan).before;
     if (at <= goal && goal < at + w) s.at = tid;
     __syncthreads();
-    found = s.hist[s.at];
+    const u64 found = s.hist[s.at];
     __syncthreads();
-    return true;
+    return found;
   }
 
   __device__ __forceinline__ void refuse(size_t at, uint32_t bit) {
@@ -806,8 +840,8 @@ struct Sampler {
         }
         __syncthreads();
         limit = ~0ull;
-        if (by_k && n >= top_k) fits = pick(weigh, n, ~0ull, false, 0, (u64)(top_k - 1), limit);
-        if (by_p && fits) {
+        if (by_k && n >= top_k) limit = pick(weigh, n, ~0ull, false, 0, (u64)(top_k - 1));
+        if (by_p) {
           u64 mass = all_mass;
           if (by_k || small) {
             u64 sum = 0;
@@ -815,14 +849,10 @@ struct Sampler {
               if (s.sorted[i] <= limit) sum += weight_of(weigh, value_of(s.sorted[i]));
             mass = block_before(sum, s.scan).all;
           }
-          u64 k = ~0ull;
-          const u64 goal = mass_goal(mass);
-          // (min-p's floor may lie above the list)
-          fits = n == 0 || pick(weigh, n, limit, true, base, goal, k);
+          // (n = 0, or no entry passes the goal: min-p's floor lies above the list)
+          const u64 k = n == 0 ? ~0ull : pick(weigh, n, limit, true, base, mass_goal(mass));
           limit = k < limit ? k : limit;
         }
-      }
-      if (fits) {
         limit = floor_key < limit ? floor_key : limit;
         for (int i = tid; i < s.listed; i += SA_THREADS) {
           const int v = s.index[i];
@@ -837,13 +867,18 @@ struct Sampler {
       }
     }
     if (listing && !fits) {
-      // ---- 2 to 4 by searches over the row
-      const u64 most = (u64)top << p.idx_bits;
+      // ---- 2 to 4 by searches over the row; with top-p alone among the keys of the window
+      const bool window = all_mass != 0;
       limit = every;
       for (int filter = by_k ? 0 : 1; filter < 3; ++filter) {  // the k-th entry, the mass of top-p, the tiles' sums
-        u64 goal = (u64)(top_k - 1), k;
-        if (filter > 0) {
-          if (filter == 2) limit = floor_key < limit ? floor_key : limit;
+        u64 lo = (u64)top << p.idx_bits, from_mass = 0, goal = (u64)(top_k - 1), k;
+        if (filter == 1 && !by_p) continue;
+        if (filter == 2) limit = floor_key < limit ? floor_key : limit;
+        if (filter == 1 && window) {
+          if (sure < INFINITY) lo = key_of(sure, 0);
+          from_mass = base;
+          goal = mass_goal(all_mass);
+        } else if (filter > 0) {
           kept = count = 0;
           u64 sum = 0;
           each_entry(
@@ -859,14 +894,15 @@ struct Sampler {
                 kept += sum;
                 sum = 0;
               });
-          if (filter == 2 || !by_p) continue;
+          if (filter == 2) break;
           const u64 here = block_before(kept, s.scan).all;
-          sync();                                         // the sums before it have been read
+          sync();                                            // the sums before it have been read
           if (tid == 0) s.sum[0] = here;
           sync();
           goal = mass_goal(warp_sum64(of_rank((u64)0, [](const SampleShared* o) { return o->sum[0]; })));
         }
-        if (search(most, limit, goal, [&](float x) { return filter == 0 ? 1ull : weight_of(weigh, x); }, k)) limit = k;
+        const u64 hi = filter == 1 && window ? key_of(low_x, 0) | mask : limit;
+        if (search(lo, hi, from_mass, goal, [&](float x) { return filter == 0 ? 1ull : weight_of(weigh, x); }, k)) limit = k;
       }
     }
 
@@ -978,11 +1014,13 @@ cudaError_t launch_sample(const spec_sample_args& a, int sms, cudaStream_t st) {
   p.less = bits > 19 ? bits - 19 : 0;
   const long long rows = (long long)a.B * a.n;
   const int size = a.dtype == SPEC_BF16 ? 2 : 4, W = 16 / size;
-  // CTAs a row: slices that stay in shared memory, and enough of them for few rows
+  // CTAs a row: more of them while all are on the GPU at once, two an SM, and have 16384
+  // entries each.  us a call, cold caches, with 1, 2, 4 and 8: 128 rows of 32000 bf16,
+  // top-k 50: 22, 27, 45, 96; 16 rows of 128256 bf16, top-p 0.9: 86, 57, 39, 39; 64 rows of
+  // 151936 fp32, top-p 0.9: 123, 78, 70, 94.
   int C = 1;
   auto slice = [&] { return ((a.V + C - 1) / C + 32 * W - 1) / (32 * W) * (32 * W); };
-  auto bytes = [&] { return (long long)(slice() + 32 * W) * size; };   // an alignment's entries more
-  while (C < 8 && (bytes() > SA_SLICE || (2 * C * rows <= 4LL * sms && a.V / (2 * C) >= 4096))) C *= 2;
+  while (C < 8 && 2 * C * rows <= 2LL * sms && a.V / (2 * C) >= 16384) C *= 2;
   while ((long long)(C - 1) * slice() >= a.V) --C;           // no empty slice
   p.slice = slice();
   // tiles of four vectors a lane where every warp has some
