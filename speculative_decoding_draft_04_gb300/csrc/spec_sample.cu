@@ -239,7 +239,7 @@ struct SampleShared {
   uint32_t count[SA_WARPS];
   int index[SA_LIST];                     // this CTA's list
 };
-constexpr int SA_STAGE = 4;               // vectors a lane staged at a time where slices do not stay
+constexpr int SA_STAGE = 4;               // vectors a lane at a time; two such stages a warp where slices do not stay
 constexpr int SA_SLICE = 69 * 1024;       // bytes of a slice that stays: two CTAs an SM
 static_assert(offsetof(SampleShared, tab) % 16 == 0 && SA_LIST % 2 == 0 && sizeof(SampleShared) % 16 == 0,
               "16 bytes at a time");
@@ -306,12 +306,9 @@ struct Sampler {
     const int own = v - (begin + (r - rank) * p.slice);
     return (float)reinterpret_cast<const DT*>(cl.map_shared_rank(data, r))[own];
   }
-  // Requests the vectors [i0, i0 + n) a lane of tile t.
-  __device__ __forceinline__ uint8_t* place(int t, int i0) const {
-    return data + (p.resident ? t * p.tile_vectors + i0 : warp * SA_STAGE) * 512;
-  }
-  __device__ __forceinline__ void request(int t, int i0, int n) const {
-    uint8_t* to = place(t, i0) + lane * 16;
+  // Requests the vectors [i0, i0 + n) a lane of tile t, to `to`.
+  __device__ __forceinline__ void request(uint8_t* to, int t, int i0, int n) const {
+    to += lane * 16;
     int v = begin + t * tile_len + (i0 * 32 + lane) * W;
 #pragma unroll 1
     for (int i = 0; i < n; ++i, v += 32 * W, to += 512) {
@@ -319,20 +316,34 @@ struct Sampler {
       else *reinterpret_cast<uint4*>(to) = load_part(v);
     }
   }
-  // f(vector, its first entry, where it is) of the CTA's entries; done(tile) after each tile.
+  // f(vector, its first entry) of the CTA's entries, SA_STAGE vectors a lane at a time;
+  // done(tile) after each tile.  Where the slice does not stay, the next vectors are on
+  // their way while some are worked on.
   template <class F, class Done>
   __device__ __forceinline__ void each_vector(F f, Done done) const {
+    const int most = min(SA_STAGE, p.tile_vectors);
+    auto stage = [&](int turn) { return data + ((turn & 1) * SA_WARPS + warp) * (SA_STAGE * 512); };
+    if (!p.resident && warp < tiles) {
+      request(stage(0), warp, 0, most);
+      cp_async_commit();
+    }
+    int turn = 0;
 #pragma unroll 1
     for (int t = warp; t < tiles; t += SA_WARPS) {
 #pragma unroll 1
-      for (int i0 = 0; i0 < p.tile_vectors; i0 += SA_STAGE) {
+      for (int i0 = 0; i0 < p.tile_vectors; i0 += SA_STAGE, ++turn) {
         const int n = min(SA_STAGE, p.tile_vectors - i0);
+        const uint8_t* at = data + (t * p.tile_vectors + i0) * 512;
         if (!p.resident) {
-          request(t, i0, n);
+          const bool same = i0 + SA_STAGE < p.tile_vectors;
+          const int next = same ? t : t + SA_WARPS, from = same ? i0 + SA_STAGE : 0;
+          __syncwarp();                                      // the buffer has been read
+          if (next < tiles) request(stage(turn + 1), next, from, min(SA_STAGE, p.tile_vectors - from));
           cp_async_commit();
-          cp_async_wait_all();                               // each lane reads what it requested
+          asm volatile("cp.async.wait_group 1;\n" ::: "memory");   // each lane reads what it requested
+          at = stage(turn);
         }
-        const uint8_t* at = place(t, i0) + lane * 16;
+        at += lane * 16;
         int v = begin + t * tile_len + (i0 * 32 + lane) * W;
         if (n == SA_STAGE) {
           uint4 q[SA_STAGE];
@@ -611,7 +622,7 @@ struct Sampler {
     const int top_k = p.top_k ? __ldg(p.top_k + b) : 0;
     if (p.resident) {                                        // (a row that is refused is not waited for)
       if (u != -1.f)
-        for (int t = warp; t < tiles; t += SA_WARPS) request(t, 0, p.tile_vectors);
+        for (int t = warp; t < tiles; t += SA_WARPS) request(data + t * p.tile_vectors * 512, t, 0, p.tile_vectors);
       cp_async_commit();
     }
     static_assert(SA_TABLE / 2 == SA_THREADS, "16 bytes of the table a thread");
@@ -1021,6 +1032,9 @@ cudaError_t launch_sample(const spec_sample_args& a, int sms, cudaStream_t st) {
   int C = 1;
   auto slice = [&] { return ((a.V + C - 1) / C + 32 * W - 1) / (32 * W) * (32 * W); };
   while (C < 8 && 2 * C * rows <= 2LL * sms && a.V / (2 * C) >= 16384) C *= 2;
+  // two a row also where that is a second wave, but the rows of one are long ones: 256 rows of
+  // 128256 bf16 of mixed settings 117 us, with one CTA a row 135 to 158
+  if (C == 1 && 2 * rows <= 4LL * sms && a.V >= 65536) C = 2;
   while ((long long)(C - 1) * slice() >= a.V) --C;           // no empty slice
   p.slice = slice();
   // tiles of four vectors a lane where every warp has some
@@ -1031,7 +1045,7 @@ cudaError_t launch_sample(const spec_sample_args& a, int sms, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * C));
   cfg.blockDim = dim3(SA_THREADS);
-  cfg.dynamicSmemBytes = sizeof(SampleShared) + (size_t)(p.resident ? whole : SA_WARPS * SA_STAGE * 512);
+  cfg.dynamicSmemBytes = sizeof(SampleShared) + (size_t)(p.resident ? whole : 2 * SA_WARPS * SA_STAGE * 512);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
