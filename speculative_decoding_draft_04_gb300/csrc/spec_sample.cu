@@ -498,7 +498,8 @@ struct Sampler {
     return k;
   }
   // Of the list's n keys up to `most`: the first whose running sum, of weights after `base`
-  // or of ones, passes `goal`.
+  // or of ones, passes `goal`; `most` where none does (fewer entries than k, or min-p's
+  // floor above the list).
   __device__ __forceinline__ u64 pick(const Weigh& weigh, int n, u64 most, bool weights, u64 base, u64 goal) {
     constexpr int PER = SA_LIST / SA_THREADS, BINS = SA_BINS / 2;
     u64 k[PER];
@@ -586,12 +587,13 @@ struct Sampler {
     __syncthreads();
     left = min(s.bin[1], SA_THREADS);
     u64 own = tid < left ? s.hist[tid] : ~0ull;
+    if (tid == 0) s.at = -1;
     own = sort_keys(own, left);
     const u64 w = own == ~0ull ? 0 : weights ? weight_of(weigh, value_of(own)) : 1;
     const u64 at = base + block_before(w, s.scan).before;
     if (at <= goal && goal < at + w) s.at = tid;
     __syncthreads();
-    const u64 found = s.hist[s.at];
+    const u64 found = s.at >= 0 ? s.hist[s.at] : most;
     __syncthreads();
     return found;
   }
@@ -704,7 +706,7 @@ struct Sampler {
     float from = least, sure = -INFINITY, low_x = SA_LOWEST, bin_scale = 0.f;
     u64 all_mass = 0, base = 0, limit = floor_key, kept = 0;   // kept: this thread's mass, in the end
     uint32_t count = 0;
-    const bool listing = by_k || by_p, small = p.V <= SA_LIST;
+    const bool listing = by_k || by_p, small = p.V < SA_LIST;
     bool fits = !by_k || top_k < SA_LIST;
     auto bin_of = [&](float x) { return min(__float2int_rz(rn_mul(rn_sub(m, x), bin_scale)), SA_BINS - 1); };
     uint32_t* bins = reinterpret_cast<uint32_t*>(s.hist);
@@ -728,7 +730,11 @@ struct Sampler {
       }
     }
     for (bool again = listing && fits && !small;;) {
-      if (!listing || (fits && (counting || !again))) {
+      if (listing && small && fits) {                        // every entry is listed, in its place
+        for (int i = tid; i < p.V; i += SA_THREADS) s.index[i] = i;
+        if (tid < tiles) s.tile[tid] = 0;
+        if (tid == 0) s.listed = p.V;
+      } else if (!listing || (fits && (counting || !again))) {
         Sum part;
         each_vector(
             [&](const uint4& q, int v, const uint8_t*) {
@@ -850,8 +856,8 @@ struct Sampler {
           s.sorted[i] = key_of(value_at(v, r), v);
         }
         __syncthreads();
-        limit = ~0ull;
-        if (by_k && n >= top_k) limit = pick(weigh, n, ~0ull, false, 0, (u64)(top_k - 1));
+        limit = every;                                       // (-inf, in small lists, comes behind)
+        if (by_k) limit = pick(weigh, n, every, false, 0, (u64)(top_k - 1));
         if (by_p) {
           u64 mass = all_mass;
           if (by_k || small) {
@@ -860,9 +866,7 @@ struct Sampler {
               if (s.sorted[i] <= limit) sum += weight_of(weigh, value_of(s.sorted[i]));
             mass = block_before(sum, s.scan).all;
           }
-          // (n = 0, or no entry passes the goal: min-p's floor lies above the list)
-          const u64 k = n == 0 ? ~0ull : pick(weigh, n, limit, true, base, mass_goal(mass));
-          limit = k < limit ? k : limit;
+          limit = pick(weigh, n, limit, true, base, mass_goal(mass));
         }
         limit = floor_key < limit ? floor_key : limit;
         for (int i = tid; i < s.listed; i += SA_THREADS) {
