@@ -692,10 +692,11 @@ int32_t spec_logprobs(const spec_logprobs_args* args, spec_stream_t stream);
  *                     the first top_k[b] lies         (1: no limit)
  * and at least one.  The token is the smallest v with F(v) > u F(V), F summing
  * the kept w in vocabulary order; logprob is log(w_v / F(V)), kept is n.
- * Arithmetic: each w is a whole number of 2^-41 of the largest (2^-(62 - bits of
- * V) for V > 2^21) within 2^-34 of its value relative, so every sum is exact, in
- * any order: a result is the same on every run, and that of the definition unless
- * a border is nearer than the weights' errors together, some 1e-12 of the mass.
+ * Arithmetic: each w, to 2^-34 relative, is rounded to a whole number of 2^-43 of
+ * the largest (2^-(62 - bits of V) for V >= 2^19), so every sum is exact, in any
+ * order: a result is the same on every run, and that of the definition unless a
+ * border is nearer than the weights' errors together (their roundings average
+ * out; entries below 2^-45 of the largest count as 0).
  * u = -1: the row is not read, its token is -1, logprob NaN, kept 0.  The same
  * outputs, with the bit, for u outside [0, 1), top_p or min_p outside [0, 1]
  * (SPEC_DEV_BAD_FILTER), a temperature not finite and > 0 (SPEC_DEV_BAD_TEMP)

@@ -7,7 +7,8 @@
 // key-value head and the new tokens are the rows of one product: row r of
 // request b is new token r / G, query head h G + r % G (G = Hq / Hkv).
 //
-// Requests of at most 32 rows on average (others: spec_attention_tc.cu).
+// Requests of at most 32 rows on average (others: spec_attention_tc.cuh).  The kernels
+// are in spec_attention_rows.cuh; spec_prefix.cu launches them for shared prefixes.
 //
 // cache_attention_kernel: every warp works alone on a run of 32-token units.
 // All units of all (request, key-value head, row tile) segments are numbered in

@@ -6,6 +6,13 @@
 // prefix as one request's that see every token, so that a token of it is decoded once
 // for 128 rows; then every request's rows over its own tokens, whose end adds the sums
 // (unnormalised, 32 bits, with their maximum) that the first pass left.
+//
+// us a call: trees of 25 nodes of 32 requests behind 32768 tokens 460, nearly
+// all of it the first pass: 0.94 PFLOP/s (225 us at the rate of a matrix product), bound
+// as the 128-row tiles are by a unit's chain of waits; blocks of 2 to 8 tokens of 128 requests in
+// four groups behind up to 8192 tokens 208; one token of 64 requests behind 16384 tokens 83
+// (35 and 37 in the two passes, the rest in their joins; 14 us of reading); one token of 4
+// requests behind 2000 tokens 26.
 #include "spec_attention_rows.cuh"
 
 namespace spec {
@@ -36,7 +43,8 @@ cudaError_t launch_prefix_attention(const spec_prefix_attention_args& a, int sms
   // prefixes always (4 requests of 4 rows behind 2000 tokens: 34 us a call, 40 with 16-row
   // tiles), for the requests' own tokens where tables have room for few (blocks of 8 to 32
   // rows behind 516 own tokens on average: 212 us, 273 with 16-row tiles; 8 rows and fewer
-  // stay with their tiles: one token of 64 requests 99 us, 124 in 128-row tiles).
+  // stay with their tiles: one token of 64 requests 99 us, 124 in 128-row tiles).  Tables of
+  // more room may hold long contexts; they keep the plain call's border.
   const cudaError_t e = launch_tiles<PASS_PREFIX>(shared, o.D, o.dtype, 8, sms, st);
   if (e != cudaSuccess) return e;
   return launch_tiles<PASS_OWN>(own, o.D, o.dtype, (long long)o.table_stride * o.page_size <= 4096 ? 8 : 32, sms, st);

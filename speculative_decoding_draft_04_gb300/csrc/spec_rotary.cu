@@ -14,7 +14,17 @@
 // describes in the cache: groups g and g + R / 32 where pairs are halves apart, so
 // that both elements of a pair are its own, neighbouring groups elsewhere.  D / 32
 // lanes share a head, a warp has 1024 / D heads of one token, and a warp that goes
-// on to more heads of its token keeps the cosines and sines.
+// on to more heads of its token keeps the cosines and sines and requests the next
+// heads before it works on the ones that it has.
+//
+// Long runs are bound by instructions and memory alike: 30011 tokens of 32 + 8 + 8 heads
+// of 128 bf16 elements move 787 MB in 166 us, 4.7 TB/s of the 6.8 of a copy, with 65 % of
+// the issue slots taken (22 instructions an element; 252 us with the sums of squares by
+// TwoSum, one group of heads a warp and nothing ahead).  1024 tokens take 12.6 us a call
+// (4.0 us of reading and writing): slot, position, rotation and head one after the other, in
+// two and a half waves of CTAs.  fp32 has no registers for heads ahead: 4099 tokens of
+// 16 + 4 + 4 heads of 256, 207 MB, take 64 us (with heads ahead 67, with five CTAs an SM
+// 74, spilling).
 #include "spec_cache.cuh"
 #include "spec_df.cuh"
 
