@@ -553,7 +553,7 @@ int32_t spec_cache_append(const spec_cache_append_args* args, spec_stream_t stre
  * position outside [0, rope_rows) (SPEC_DEV_BAD_POSITION): nothing is written
  * into the cache for the row, its q_out is NaN, the values as stored are zeros.
  * Keys and values that are not finite are stored as in spec_cache_append
- * (SPEC_DEV_BAD_KV).
+ * (SPEC_DEV_BAD_KV); two rows with one slot leave parts of both there.
  * q_out may be q itself (the same address and strides); no other output may
  * overlap an input.  Strides as in spec_cache_append, q_out's too; the limits
  * of spec_cache_append, and 1 <= Hq <= 256, (T + 16) Hq D < 2^36, R a multiple of

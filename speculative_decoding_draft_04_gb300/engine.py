@@ -432,6 +432,8 @@ class Prefixes:
     def allocate(cls, c: DeviceCache, group_sizes, Hq) -> "Prefixes":
         import torch
         groups, requests = len(group_sizes), sum(group_sizes)
+        if requests < 1 or min(group_sizes) < 0:
+            raise _lib.SpecError(f"groups of {list(group_sizes)} requests")
         if requests + groups != c.kv_len.numel():
             raise _lib.SpecError(f"{groups} groups of {requests} requests need a cache of {requests + groups}, "
                                  f"not {c.kv_len.numel()}")
