@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_attention_join_kernel(cons
   __shared__ float4 s_acc[JOIN_THREADS];
   __shared__ float2 s_ml[JOIN_THREADS];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  if (PASS == PASS_PREFIX) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   constexpr int PART = ROWS * D + 2 * ROWS, RQ = D / 4;      // float4 a row
   constexpr int JOIN_ROWS = JOIN_THREADS / RQ < ROWS ? JOIN_THREADS / RQ : ROWS;
   const float* parts = attn_parts(p);
@@ -430,20 +431,42 @@ __global__ void __launch_bounds__(JOIN_THREADS) cache_attention_join_kernel(cons
   }
 }
 
-// Launches the join after the main kernel of `ctas` CTAs x `per_cta` workers;
-// its launch overlaps the main kernel's end.
-template <int PASS, int D, int ROWS, class DT>
-cudaError_t launch_attention_join(const AttnParams& p, int workers, int sms, cudaStream_t st) {
+// A kernel whose launch overlaps the end of the one before it.
+inline cudaError_t launch_overlapping(const void* kernel, dim3 grid, int threads, size_t smem, cudaStream_t st, void** args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(workers < 4 * sms ? workers : 4 * sms, (ROWS * D / 4 + JOIN_THREADS - 1) / JOIN_THREADS);
-  cfg.blockDim = dim3(JOIN_THREADS);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_attention_join_kernel<PASS, D, ROWS, DT>, p, workers);
+  return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+// The main kernel of a pass.  That over own tokens numbers its work while the prefixes'
+// parts are still being joined, and waits before it reads or writes what that kernel does
+// (4 requests behind 2000 tokens 26 us a call, 23 so; 64 behind 16384 83 and 79).
+template <int PASS>
+cudaError_t launch_main(void (*kernel)(AttnParams), const AttnParams& p, int ctas, int threads, size_t smem, cudaStream_t st) {
+  if (PASS == PASS_OWN) {
+    void* args[] = {const_cast<AttnParams*>(&p)};
+    return launch_overlapping(reinterpret_cast<const void*>(kernel), dim3(ctas), threads, smem, st, args);
+  }
+  kernel<<<ctas, threads, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+// Launches the join after the main kernel of `ctas` CTAs x `per_cta` workers;
+// its launch overlaps the main kernel's end.
+template <int PASS, int D, int ROWS, class DT>
+cudaError_t launch_attention_join(const AttnParams& p, int workers, int sms, cudaStream_t st) {
+  const dim3 grid(workers < 4 * sms ? workers : 4 * sms, (ROWS * D / 4 + JOIN_THREADS - 1) / JOIN_THREADS);
+  void* args[] = {const_cast<AttnParams*>(&p), &workers};
+  return launch_overlapping(reinterpret_cast<const void*>(&cache_attention_join_kernel<PASS, D, ROWS, DT>), grid,
+                            JOIN_THREADS, 0, st, args);
 }
 
 }  // namespace spec

@@ -577,6 +577,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, C::MIN_CTAS) cache_attention_ke
   if (lane < F::DEPTH) mbar_init(bar + lane, 1);
   const long long total = attn_prefix<C::PASS, C::ROWS, AT_UNIT, 32 * C::WARPS>(p, s_pre, s_scan, [] { __syncthreads(); });
   __syncthreads();
+  if (C::PASS == PASS_OWN) asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
   const int workers = gridDim.x * C::WARPS, me = warp * gridDim.x + blockIdx.x;
@@ -787,8 +788,8 @@ cudaError_t launch_cfg(const AttnParams& p, int sms, cudaStream_t st) {
   const long long tiles = (long long)p.T * p.G / C::ROWS + (p.T < p.B ? p.T : p.B);
   const long long units = tiles * p.Hkv * (((long long)p.stride * p.P + AT_UNIT - 1) / AT_UNIT);
   if (ctas > units) ctas = units;
-  cache_attention_kernel<C, DT><<<(int)ctas, 32 * C::WARPS, F::SMEM, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_main<C::PASS>(cache_attention_kernel<C, DT>, p, (int)ctas, 32 * C::WARPS, F::SMEM, st);
+  if (e != cudaSuccess) return e;
   return launch_attention_join<C::PASS, C::D, C::ROWS, DT>(p, (int)ctas * C::WARPS, sms, st);
 }
 }  // namespace

@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(TA_THREADS, 2) cache_attention_tc_kernel(const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (PASS == PASS_OWN) asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const long long total = s_pre[TA_PREFIX];
   const uint32_t tmem = s_tmem;
@@ -619,8 +620,8 @@ cudaError_t launch_tc(const AttnParams& p, int sms, cudaStream_t st) {
   long long ctas = 2LL * sms;
   if (ctas > AT_MAX_CTAS) ctas = AT_MAX_CTAS;
   if (ctas > units) ctas = units;
-  cache_attention_tc_kernel<PASS, D><<<(int)ctas, TA_THREADS, L::TOTAL, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_main<PASS>(cache_attention_tc_kernel<PASS, D>, p, (int)ctas, TA_THREADS, L::TOTAL, st);
+  if (e != cudaSuccess) return e;
   return launch_attention_join<PASS, D, TA_ROWS, bf16>(p, (int)ctas, sms, st);
 }
 }  // namespace

@@ -7,12 +7,12 @@
 // for 128 rows; then every request's rows over its own tokens, whose end adds the sums
 // (unnormalised, 32 bits, with their maximum) that the first pass left.
 //
-// us a call: trees of 25 nodes of 32 requests behind 32768 tokens 460, nearly
-// all of it the first pass: 0.94 PFLOP/s (225 us at the rate of a matrix product), bound
-// as the 128-row tiles are by a unit's chain of waits; blocks of 2 to 8 tokens of 128 requests in
-// four groups behind up to 8192 tokens 208; one token of 64 requests behind 16384 tokens 83
+// us a call: trees of 25 nodes of 32 requests behind 32768 tokens 457, nearly all of it
+// the first pass: 0.95 PFLOP/s (225 us at the rate of a matrix product), bound as the
+// 128-row tiles are by a unit's chain of waits; blocks of 2 to 8 tokens of 128 requests in
+// four groups behind up to 8192 tokens 203; one token of 64 requests behind 16384 tokens 79
 // (35 and 37 in the two passes, the rest in their joins; 14 us of reading); one token of 4
-// requests behind 2000 tokens 26.
+// requests behind 2000 tokens 23.
 #include "spec_attention_rows.cuh"
 
 namespace spec {
