@@ -119,8 +119,8 @@ __device__ const PowerTable g_powers = power_table();
 // sum of two million random weights).  Entries below 2^-45 count as nothing.
 //
 // A weight comes as two 32-bit numbers, of units 2^-22 and 2^-43 (signed), that adding
-// 3 and 1.5 2^-20 leaves in the low bits of fp32 numbers: up to 1023 weights add up in
-// 32 bits, offsets and all.  Two weights at a time, by instructions of two numbers.
+// 3 and 1.5 2^-20 leaves in the low bits of fp32 numbers: the second one is at most 2^20 in
+// size, so up to 2047 weights add up in 32 bits without their offsets.  Two weights at a time, by instructions of two numbers.
 struct Weights2 {
   uint32_t a[2], b[2];                    // offset by WEIGHT_A and WEIGHT_B
 };
@@ -1047,6 +1047,8 @@ cudaError_t launch_sample(const spec_sample_args& a, int sms, cudaStream_t st) {
   // two a row also where that is a second wave, but the rows of one are long ones: 256 rows of
   // 128256 bf16 of mixed settings 117 us, with one CTA a row 135 to 158
   if (C == 1 && 2 * rows <= 4LL * sms && a.V >= 65536) C = 2;
+  // a lane of a tile adds at most 1024 weights, whose low parts (to 2^20 each) fit 32 bits
+  while (slice() > 1 << 22) C *= 2;
   while ((long long)(C - 1) * slice() >= a.V) --C;           // no empty slice
   p.slice = slice();
   // tiles of four vectors a lane where every warp has some
