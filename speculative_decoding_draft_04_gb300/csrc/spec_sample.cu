@@ -835,6 +835,9 @@ struct Sampler {
           const float x = m - ((float)first_bin - o) * step;
           if (bin_of(x) < first_bin) sure = x;
         }
+        // down to the type's next number: the same entries lie above it, and its key (of 16 bits) is its own,
+        // which a search begins with
+        if (sizeof(DT) == 2) sure = __bfloat162float(__float2bfloat16_rd(sure));
         from = least > sure ? least : nextafterf(sure, INFINITY);   // (where min-p takes some away, its floor is the limit)
       }
       const int last_bin = s.bin[1];
