@@ -116,7 +116,7 @@ __device__ const PowerTable g_powers = power_table();
 // whole number and y = t - k, and 2^(t/1024) = 2^(k/1024) (1 + s + s^2 / 2),
 // s = y ln 2 / 1024, whose next term is 2^-37 at most; with the table's two terms that
 // leaves a relative error below 2^-34, of either sign (it averages out: 1e-14 of the
-// sum of two million random weights).  Entries below 2^-45 count as nothing.
+// sum of two million random weights).  Entries below 2^-44.1 count as nothing: less than half a unit.
 //
 // A weight comes as two 32-bit numbers, of units 2^-22 and 2^-43 (signed), that adding
 // 3 and 1.5 2^-20 leaves in the low bits of fp32 numbers: the second one is at most 2^20 in
@@ -141,11 +141,13 @@ struct Weigh {
     inv = dd_recip(fmaxf(T, 0x1p-100f));
     c = dd_mul(inv, octaves());
     one = 0x3f800000u - ((uint32_t)less << 23);
-    low = fmaxf(m - fminf(45.5f * 1024.f / c.hi, -SA_LOWEST), SA_LOWEST);
-    if (low == m && m > SA_LOWEST) {                         // T below the entries' resolution
-      low = nextafterf(m, -INFINITY);
-      c = {46.f * 1024.f / (m - low), 0.f};
-    }
+    // rounded away from m: whatever lies lower is given the weight of `low`, which has to be 0
+    low = fmaxf(__fsub_rd(m, fminf(44.1f * 1024.f / c.hi, -SA_LOWEST)), SA_LOWEST);
+    // A distance that leaves the exponents' range: `low` is the number next to m (T is below the
+    // logits' resolution), or m = -(2^k - 1 unit in the last place) and the number between them, of 0.4
+    // to 2 units, gets 2.
+    const float most = (float)(126 - less) * 1024.f;
+    if ((m - low) * c.hi > most) c = {most / (m - low), 0.f};
   }
   __device__ __forceinline__ static df octaves() { return {1477.31970f, 1.97218615e-05f}; }   // 1024 log2(e)
   // (x - m) / T
