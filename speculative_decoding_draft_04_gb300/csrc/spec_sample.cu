@@ -407,10 +407,13 @@ struct Sampler {
     return lane < C ? f(cl.map_shared_rank(&s, lane)) : none;
   }
 
-  // Adds w to a 64-bit bin, once for the lanes that add the same to the same one: 64-bit
-  // additions to one address go one after the other, and ties send thousands there.
-  __device__ __forceinline__ void add_to_bin(int bin, u64 w) const {
-    const uint32_t same = __match_any_sync(__activemask(), ((u64)bin << 44) | w);
+  // Lanes that are `in` add w to a 64-bit bin, once for those that add the same to the same one:
+  // 64-bit additions to one address go one after the other, and ties send thousands there.  Called
+  // by whole warps: the lanes that match one another are those of the ballot.
+  __device__ __forceinline__ void add_to_bin(bool in, int bin, u64 w) const {
+    const uint32_t lanes = __ballot_sync(0xffffffffu, in);
+    if (!in) return;
+    const uint32_t same = __match_any_sync(lanes, ((u64)bin << 44) | w);
     if (__ffs(same) - 1 == lane) atomicAdd(&s.hist[bin], w * __popc(same));
   }
   __device__ __forceinline__ void clear_bins() {
@@ -438,12 +441,22 @@ struct Sampler {
       sync();                                             // the bins have been read
       clear_bins();
       __syncthreads();
-      each_entry(
-          [&](float x, int v) {
-            const u64 k = key_of(x, v);
-            if (k >= lo && k <= hi) {
-              const u64 w = weight(x);
-              if (w) add_to_bin((int)((k - lo) >> shift), w);
+      each_vector(
+          [&](const uint4& q, int v, const uint8_t* at) {
+            bool some = false;
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+              const u64 k = key_of(entry(q, e), v + e);
+              some |= k >= lo && k <= hi;
+            }
+            if (!__any_sync(0xffffffffu, some)) return;
+#pragma unroll 1
+            for (int e = 0; e < W; ++e) {
+              const float x = (float)reinterpret_cast<const DT*>(at)[e];
+              const u64 k = key_of(x, v + e);
+              u64 w = 0;
+              if (k >= lo && k <= hi) w = weight(x);
+              add_to_bin(w != 0, (int)((k - lo) >> shift), w);
             }
           },
           [](int) {});
@@ -554,7 +567,7 @@ struct Sampler {
       };
 #pragma unroll
       for (int i = 0; i < PER; ++i)
-        if (k[i] != ~0ull) add_to_bin(bin_of(k[i]), weights ? weight_of(weigh, value_of(k[i])) : 1ull);
+        add_to_bin(k[i] != ~0ull, bin_of(k[i]), k[i] == ~0ull ? 0 : weights ? weight_of(weigh, value_of(k[i])) : 1ull);
       if (tid == 0) {
         s.bin[0] = -1;
         s.bin[1] = 0;
