@@ -343,6 +343,7 @@ class DeviceCache:
     positions: object
     status: object
     workspace: object
+    steps: int = 0          # calls of make_room
 
     @classmethod
     def allocate(cls, B, layers, Hq, Hkv, D, page_size, num_pages, max_tokens, max_rows, k_scale,
@@ -392,6 +393,7 @@ def make_room(c: DeviceCache, new_len, accept_len=None, stream=None) -> None:
                            c.ring_pos[new], c.row_ptr, c.slots, c.positions, c.status, c.page_size,
                            stream=stream)
     c.newest = new
+    c.steps += 1
 
 
 @dataclasses.dataclass
@@ -427,6 +429,7 @@ class Prefixes:
     group: object               # int64 [requests]: the group of each request
     positions: object           # int32 [max_rows]: positions that count the prefix
     workspace: object
+    placed: int = -1            # the cache's step that they are of
 
     @classmethod
     def allocate(cls, c: DeviceCache, group_sizes, Hq) -> "Prefixes":
@@ -460,6 +463,7 @@ def place_after(c: DeviceCache, s: Prefixes, stream=None) -> None:
         who = torch.searchsorted(c.row_ptr[1:s.requests + 1].long(), row, right=True).clamp(max=s.requests - 1)
         before = c.kv_len[s.requests:][s.group[who]]
         torch.where(c.positions < 0, c.positions, c.positions + before, out=s.positions)
+    s.placed = c.steps
 
 
 def attend(c: DeviceCache, layer: int, q, k, v, out, tree_mask=None, lse=None, stream=None,
@@ -469,8 +473,11 @@ def attend(c: DeviceCache, layer: int, q, k, v, out, tree_mask=None, lse=None, s
     with T at most the rows that the step was made for.  rotary: queries (in
     place) and keys are normed and rotated first.  prefixes: the rows are the
     sharing requests' (the holders have none in this step), each sees its
-    group's prefix before its own tokens."""
+    group's prefix before its own tokens.  With both, place_after has to have
+    followed this step's make_room: positions of another step are refused."""
     T = k.shape[0]
+    if rotary is not None and prefixes is not None and prefixes.placed != c.steps:
+        raise _lib.SpecError("the prefixes' positions are of another step: place_after follows make_room")
     if rotary is None:
         _lib.spec_cache_append(k, v, c.slots[:T], c.layers[layer], c.status, c.k_scale[layer],
                                c.v_scale[layer], stream=stream)
