@@ -640,7 +640,7 @@ int32_t spec_cache_attention(const spec_cache_attention_args* args, spec_stream_
  * outside the cache SPEC_DEV_BAD_SLOT: the group's rows get NaN; of a bad page
  * at least those of its row tile).  With group_ptr's first or last entry wrong, or
  * entries that do not ascend, every row of every request gets NaN.
- * 0 <= groups <= 4096, groups * prefix_stride < 2^31; workspace
+ * 1 <= groups <= 4096, prefix_stride >= 1, groups * prefix_stride < 2^31; workspace
  * spec_prefix_attention_workspace_bytes(T, Hq, Hkv, D) bytes.                */
 typedef struct {
   spec_cache_attention_args own;
