@@ -163,6 +163,7 @@ template <int PASS_, int D_, int M_, int NT_>
 struct RowTiles {
   using C = RowTiles;
   static constexpr bool FRESH = NT_ == 2 && PASS_ != PASS_PLAIN;
+  static_assert(PASS_ != PASS_PREFIX || D_ == 256 || NT_ == 2, "bf16 rows of groups: 8-row or 128-row tiles");
   static constexpr int PASS = PASS_, D = D_, M = M_, NT = NT_, ROWS = 16 * M;
   static constexpr int KSTEPS = D / 16, KW = D / 32, KG = D / 64, NV = D / 8, VW = D >= 128 ? D / 64 : 1;
   static constexpr int Q_BYTES = NT * ROWS * KSTEPS * 32;
@@ -803,7 +804,7 @@ inline AttnParams own_params(const spec_cache_attention_args& a) {
                     cache_attention_scale(a), a.v_scale, a.out, a.lse, a.dev_status, a.workspace};
 }
 
-// tc_from: 128-row tiles from more rows a request on.
+// tc_from: 128-row tiles from more rows a request on (PASS_PREFIX: 8).
 template <int PASS>
 cudaError_t launch_tiles(const AttnParams& p, int D, int dtype, int tc_from, int sms, cudaStream_t st) {
   // The tile by the mean rows a request (finished requests and rows of no request
@@ -832,14 +833,19 @@ cudaError_t launch_tiles(const AttnParams& p, int D, int dtype, int tc_from, int
   //     379, 235 against 211, 1120, 596.  At 32 rows (b) 347, (c) 219 lose to 305
   //     and 170, and only (a) would gain (64 against 83).
   if (D <= 128 && rows > (long long)tc_from * p.B) return launch_cache_attention_tc<PASS>(p, D, sms, st);
-  if (D == 64)
-    return few    ? launch_cfg<ColumnTile<PASS, 64, 1>, bf16>(p, sms, st)
-           : wide ? launch_cfg<RowTiles<PASS, 64, 2, 1>, bf16>(p, sms, st)
-                  : launch_cfg<RowTiles<PASS, 64, 1, 1>, bf16>(p, sms, st);
-  if (D == 128)
-    return few    ? launch_cfg<ColumnTile<PASS, 128, 1>, bf16>(p, sms, st)
-           : wide ? launch_cfg<RowTiles<PASS, 128, 2, 1>, bf16>(p, sms, st)
-                  : launch_cfg<RowTiles<PASS, 128, 1, 1>, bf16>(p, sms, st);
+  if constexpr (PASS == PASS_PREFIX) {                       // more rows than 8 went to the 128-row tiles
+    if (D == 64) return launch_cfg<ColumnTile<PASS, 64, 1>, bf16>(p, sms, st);
+    if (D == 128) return launch_cfg<ColumnTile<PASS, 128, 1>, bf16>(p, sms, st);
+  } else {
+    if (D == 64)
+      return few    ? launch_cfg<ColumnTile<PASS, 64, 1>, bf16>(p, sms, st)
+             : wide ? launch_cfg<RowTiles<PASS, 64, 2, 1>, bf16>(p, sms, st)
+                    : launch_cfg<RowTiles<PASS, 64, 1, 1>, bf16>(p, sms, st);
+    if (D == 128)
+      return few    ? launch_cfg<ColumnTile<PASS, 128, 1>, bf16>(p, sms, st)
+             : wide ? launch_cfg<RowTiles<PASS, 128, 2, 1>, bf16>(p, sms, st)
+                    : launch_cfg<RowTiles<PASS, 128, 1, 1>, bf16>(p, sms, st);
+  }
   return few ? launch_cfg<ColumnTile<PASS, 256, 1>, bf16>(p, sms, st) : launch_cfg<RowTiles<PASS, 256, 1, 1>, bf16>(p, sms, st);
 }
 
