@@ -703,7 +703,7 @@ int32_t spec_logprobs(const spec_logprobs_args* args, spec_stream_t stream);
  * and a row with a NaN, +inf or only -inf (SPEC_DEV_BAD_LOGIT).
  * Rows: element (b, j, v) at logits[b * b_stride + j * row_stride + v]; any V,
  * strides and address of an element.  1 <= B * n <= 2^20, 1 <= V < 2^24.
- * Temperatures below 2^-100 count as that.                                   */
+ * Temperatures below 2^-100 count as that, above 2^104 as that.               */
 typedef struct {
   int32_t B, n, V, dtype;
   const void* logits;

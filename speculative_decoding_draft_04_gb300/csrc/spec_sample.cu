@@ -138,7 +138,7 @@ struct Weigh {
   df c, inv;                              // 1024 log2(e) / T, 1 / T
   const float2* tab;
   __device__ __forceinline__ Weigh(float m_, float T, int less, const float2* tab_) : m(m_), tab(tab_) {
-    inv = dd_recip(fmaxf(T, 0x1p-100f));
+    inv = dd_recip(T);
     c = dd_mul(inv, octaves());
     one = 0x3f800000u - ((uint32_t)less << 23);
     // rounded away from m: whatever lies lower is given the weight of `low`, which has to be 0
@@ -707,12 +707,15 @@ struct Sampler {
       return refuse(at, SPEC_DEV_BAD_LOGIT);
     }
     m = of_descending<DT>(top);
-    const Weigh weigh(m, T, p.less, s.tab);
+    // Above 2^104 the second term of 1 / T would lose bits below the smallest numbers (a weight's 2^-34 needs
+    // 18 of them), and from 2^123 on the cut-off, 31 T below the largest logit, would leave the type.
+    const float temp = fminf(fmaxf(T, 0x1p-100f), 0x1p104f);
+    const Weigh weigh(m, temp, p.less, s.tab);
 
     // the smallest logit that min-p keeps
     float least = SA_LOWEST;
     if (min_p > 0.f) {
-      const df edge = dd_add_f(dd_mul_f(log_of(df{min_p, 0.f}, s.tab), T), m);
+      const df edge = dd_add_f(dd_mul_f(log_of(df{min_p, 0.f}, s.tab), temp), m);
       if (edge.hi > least) least = edge.lo > 0.f ? nextafterf(edge.hi, INFINITY) : edge.hi;
     }
     if (sizeof(DT) == 2) least = __bfloat162float(__float2bfloat16_ru(least));
