@@ -715,7 +715,11 @@ struct Sampler {
     // the smallest logit that min-p keeps
     float least = SA_LOWEST;
     if (min_p > 0.f) {
-      const df edge = dd_add_f(dd_mul_f(log_of(df{min_p, 0.f}, s.tab), temp), m);
+      // (log_of takes numbers whose reciprocal is one: smaller ones times 2^60, and 60 ln 2 off again)
+      const bool tiny = min_p < 0x1p-100f;
+      df l = log_of(df{tiny ? rn_mul(min_p, 0x1p60f) : min_p, 0.f}, s.tab);
+      if (tiny) l = dd_add(l, df{-41.58883f, -1.7930694e-06f});
+      const df edge = dd_add_f(dd_mul_f(l, temp), m);
       if (edge.hi > least) least = edge.lo > 0.f ? nextafterf(edge.hi, INFINITY) : edge.hi;
     }
     if (sizeof(DT) == 2) least = __bfloat162float(__float2bfloat16_ru(least));

@@ -1,5 +1,8 @@
-"""Sampling at the ends of its arguments' ranges: temperatures above 2^104, which count as that.  Tokens,
-counts and log probabilities against float64, with the tolerances of test_sample_gpu."""
+"""Sampling at the ends of its arguments' ranges: temperatures above 2^104, which count as that, and
+min_p below the normal numbers.  Tokens, counts and log probabilities against float64, with the tolerances
+of test_sample_gpu."""
+import math
+
 import numpy as np
 import pytest
 
@@ -27,3 +30,18 @@ def test_largest_temperatures(torch, T):  # noqa: F811
             assert near > 2.0 ** -32.9 or near == 0.0
             assert st == 0 and (tokens[0, 0], kept[0, 0]) == (want, wk), (T, f, tokens, want, kept, wk)
             assert abs(lp[0, 0] - wl) <= 2.0 ** -23 * abs(wl) + 2.0 ** -31
+
+
+@pytest.mark.parametrize("min_p", [1e-37, 1.6e-38, 1e-38, 1e-39, 1e-41, 1e-44, 2e-45])
+def test_smallest_min_p(torch, min_p):  # noqa: F811
+    """Logits a few units in the last place around T ln(min_p)."""
+    min_p = float(np.float32(min_p))
+    for T in (1.0, 0.3, 7.0):
+        T = float(np.float32(T))
+        edge = np.float32(T * math.log(min_p))
+        x = (edge + np.spacing(np.abs(edge)) * np.arange(-20, 21)).astype(np.float32)
+        x = np.concatenate([[np.float32(0)], x])
+        inside = np.longdouble(x) / np.longdouble(T) - np.log(np.longdouble(min_p))
+        assert (np.abs(inside) > 1e-9).all()
+        tokens, _, kept, st = run(torch, H.dev(x[None, None]), [0.5], T, None, None, min_p)
+        assert st == 0 and tokens[0, 0] == 0 and kept[0, 0] == (inside >= 0).sum(), (T, kept, (inside >= 0).sum())
