@@ -555,7 +555,8 @@ int32_t spec_cache_append(const spec_cache_append_args* args, spec_stream_t stre
  * Keys and values that are not finite are stored as in spec_cache_append
  * (SPEC_DEV_BAD_KV); two rows with one slot leave parts of both there.
  * q_out may be q itself (the same address and strides); no other output may
- * overlap an input.  Strides as in spec_cache_append, q_out's too; the limits
+ * overlap an input.  Strides as in spec_cache_append, q_out's too, whose rows and
+ * heads may not overlap each other; the limits
  * of spec_cache_append, and 1 <= Hq <= 256, (T + 16) Hq D < 2^36, R a multiple of
  * 32 with 32 <= R <= D, 1 <= rope_rows < 2^31, eps >= 0 and finite.  Weights
  * are of dtype.                                                              */

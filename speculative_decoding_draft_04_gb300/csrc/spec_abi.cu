@@ -891,6 +891,17 @@ int32_t spec_prefix_attention(const spec_prefix_attention_args* a, spec_stream_t
   return launch_prefix_attention(*a, sms, st) == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }
 
+// Whether [n][m][D] elements by these strides are as many addresses: one dimension within a step of the other.
+static bool rows_apart(int64_t n, int64_t row, int64_t m, int64_t head, int64_t D) {
+  const auto size = [](int64_t x) { return x < 0 ? 0 - (uint64_t)x : (uint64_t)x; };
+  const auto within = [&](int64_t inner, uint64_t step, int64_t outer, uint64_t far) {
+    if (inner > 1 && step < (uint64_t)D) return false;
+    if (outer == 1) return true;
+    return far >= (uint64_t)D && (inner == 1 || (far - D) / (uint64_t)(inner - 1) >= step);
+  };
+  return within(m, size(head), n, size(row)) || within(n, size(row), m, size(head));
+}
+
 int32_t spec_rotary_append(const spec_rotary_append_args* a, spec_stream_t stream) {
   if (!a) return SPEC_EINVAL;
   if (a->T < 0 || a->T >= (1 << 24) || a->Hq < 1 || a->Hq > 256 || a->Hkv < 1 || a->Hkv > 256 || a->num_pages < 1 ||
@@ -915,6 +926,7 @@ int32_t spec_rotary_append(const spec_rotary_append_args* a, spec_stream_t strea
   // in place, every element is written by the thread that read it; otherwise not at all
   if (a->q_out == a->q && (a->q_out_row_stride != a->q_row_stride || a->q_out_head_stride != a->q_head_stride))
     return SPEC_EINVAL;
+  if (!rows_apart(a->T, a->q_out_row_stride, a->Hq, a->q_out_head_stride, a->D)) return SPEC_EINVAL;
   const int sms = num_sms();
   if (sms <= 0) return SPEC_ECUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
