@@ -539,8 +539,9 @@ int32_t spec_cache_append(const spec_cache_append_args* args, spec_stream_t stre
 
 /* spec_rotary_append: the rows of T tokens' queries, keys and values made
  * ready for attention in one pass.  With a weight, each head x of q (k) is
- * normed: y = (x inv) w, inv = 1 / sqrt(mean x^2 + eps) rounded to fp32, both
- * products rounded in fp32; without one y = x.  Its first R elements are then
+ * normed: y = (x inv) w, inv = 1 / sqrt(mean x^2 + eps) rounded to fp32 (to a
+ * number next to it where it lies within 2^-19 of a unit in the last place of a
+ * midpoint), both products rounded in fp32; without one y = x.  Its first R elements are then
  * rotated by the token's row of `rope` (pair i: c = rope[position][i][0],
  * s = rope[position][i][1]): y_a c - y_b s and y_b c + y_a s, every product and
  * sum rounded in fp32, where pair i is elements i and i + R / 2, or 2 i and

@@ -6,9 +6,10 @@
 //   inv = 1 / sqrt(mean x^2 + eps),  y = (x inv) w
 //   y_a' = y_a c - y_b s,  y_b' = y_b c + y_a s
 //
-// The sum of squares is kept in double-float and inv is its rounded reciprocal root,
-// so that all of it has one value in fp32 whatever the order of the sum: a 4-bit code
-// is decided by the last bit of a key that lies next to a border.
+// The sum of squares is kept to about 2^-48 of itself and inv is its reciprocal root by one Newton
+// step, so that inv is the nearest fp32 number unless the exact one lies within 2^-19 of a unit in the last
+// place of a midpoint (4 of 12.8 million random heads): a 4-bit code is decided by the last bit of a key
+// that lies next to a border.
 //
 // A thread has 32 elements of a head, two groups of 16 that one scale each
 // describes in the cache: groups g and g + R / 32 where pairs are halves apart, so
@@ -21,10 +22,11 @@
 // of 128 bf16 elements move 787 MB in 166 us, 4.7 TB/s of the 6.8 of a copy, with 65 % of
 // the issue slots taken (22 instructions an element; 252 us with the sums of squares by
 // TwoSum, one group of heads a warp and nothing ahead).  1024 tokens take 12.6 us a call
-// (4.0 us of reading and writing): slot, position, rotation and head one after the other, in
-// two and a half waves of CTAs.  fp32 has no registers for heads ahead: 4099 tokens of
-// 16 + 4 + 4 heads of 256, 207 MB, take 64 us (with heads ahead 67, with five CTAs an SM
-// 74, spilling).
+// (4.0 us of reading and writing): the heads are requested first, slot and position beside them, and
+// only the rotation's row waits for the position; small CTAs in two and a half waves.  fp32 has no
+// registers for heads ahead, so a warp has nothing in flight while it computes: 4099 tokens of
+// 16 + 4 + 4 heads of 256, 207 MB, take 64 us (with heads ahead in registers 67, with five CTAs an SM
+// 74, spilling); 1024 tokens of 32 + 8 + 8 heads of 128 23 us, 15000 of them 205, of 7.7 and 112.
 #include "spec_cache.cuh"
 #include "spec_df.cuh"
 
@@ -53,8 +55,8 @@ constexpr int ROTARY_THREADS = 128;
 __device__ __forceinline__ float rounded_to(const bf16*, float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
 __device__ __forceinline__ float rounded_to(const float*, float x) { return x; }
 
-// 1 / sqrt(v) rounded, from the approximate root by one Newton step whose residual
-// 1 - v r^2 is formed in double-float.
+// 1 / sqrt(v), from the approximate root by one Newton step whose residual 1 - v r^2 is formed in
+// double-float: off by 1.5 d^2 (d at most 2^-22, the root's error) before its rounding.
 __device__ __forceinline__ float root_reciprocal(df v) {
   const float r = rsqrtf(v.hi);
   const df p = dd_mul(v, two_prod_df(r, r));
@@ -64,8 +66,8 @@ __device__ __forceinline__ float root_reciprocal(df v) {
 
 // The sum of a head's squares over its LANES lanes, 32 elements each, in double-float.
 // A plain sum first gives a power of two s0 above twice the sum.  Added to s0, every
-// partial sum stays within [s0, 2 s0), so what an addition rounds away is exact as
-// fma(x, x, s - s'), and the partial sums less s0 add up without rounding.
+// partial sum stays within [s0, 2 s0): what an addition rounds away, fma(x, x, s - s'), is itself
+// rounded to about 2^-48 of the sum, and the partial sums less s0 add up without rounding.
 template <int LANES>
 __device__ __forceinline__ df sum_of_squares(const float (&a)[16], const float (&b)[16]) {
   float pa = 0.f, pb = 0.f;

@@ -23,16 +23,18 @@
 // slice in L2 cost about as much as reading it from memory).  Larger ones are staged
 // anew in every pass, the next vectors on their way while some are worked on.
 //
-// Rows whose list overflows (2048 entries next to a border: wide ties) find their
-// borders by histograms over the row itself, 1024 bins of keys a pass.
+// Rows whose list overflows (2048 entries next to a border: wide ties, flat rows of few values) and those
+// with top_k from 2048 on find their borders by histograms over the row itself, 1024 bins of keys a pass.
 //
 // Bound by instructions where every weight is needed (no filter, or top-p alone: some
 // 40 slots an entry, of which the weight's double-float argument, table and two numbers
-// are 30), by the chain of steps elsewhere: 16 rows of 128256 take 16 us with min-p
-// 0.05, 23 with top-k 50, 41 with top-p 0.9, 21 without a filter.  256 rows of
-// 128256 bf16 of mixed settings take 115 us (10 us of reading), 128 of 32000 38 us, 64 of
+// are 30), by the chain of steps elsewhere: 16 rows of 128256 take 19 us with min-p
+// 0.05, 25 with top-k 50, 56 with top-p 0.9, 23 without a filter.  256 rows of
+// 128256 bf16 of mixed settings take 117 us (10 us of reading), 128 of 32000 39 us, 64 of
 // 151936 fp32 at temperatures alone 41 us, 4 of 1000 13 to 22 us.  By one kind of filter,
-// 256 rows of 128256: none 88 us, top-k 50 68, min-p 0.05 49, top-p 0.9 154.
+// 256 rows of 128256: none 91 us, top-k 50 68, min-p 0.05 52, top-p 0.9 175 (fp32 111, 89, 72, 195);
+// by searches over the row 539 with top-k 5000, and 588 with top-p 0.9 of logits around -10, whose lists
+// overflow.
 #include <cooperative_groups.h>
 
 #include <atomic>
